@@ -254,7 +254,7 @@ def _library(s):
         from sparse_moe_expert_gemv_b200 import binding as B
         ctx = B.moe_create(2048, 768, 512, 10, B.MOE_Q4_SYM_G32_F16)
         B.moe_attn_configure(ctx, c["n_q"], c["n_kv"], c["dim"], c["page"],
-                             B.MOE_KV_E4M3 if c["cache"] == "e4m3" else B.MOE_KV_BF16, 64)
+                             B.MOE_KV_E4M3 if c["cache"] == "e4m3" else B.MOE_KV_BF16)
         _ctx[key] = (B, ctx)
     return _ctx[key]
 

@@ -19,6 +19,8 @@ enum : int {
   kErrBadSlot = 1 << 1,    // residency slot outside the slot pool
   kErrJobOverflow = 1 << 2,
   kErrTimeout = 1 << 3,    // a bounded wait gave up
+  kErrBadPage = 1 << 4,    // a page id outside the cache
+  kErrBadBatch = 1 << 5,   // row offsets or lengths that contradict the call's sizes
 };
 
 // ------------------------------------------------------------ format layout
