@@ -328,6 +328,115 @@ MOE_API moe_status moe_ep_combine(moe_ctx *ctx, int N, const float *w_dev, const
                                   const int32_t *row_of_dev, const float *y_shared_dev, void *x_dev,
                                   float *delta_dev, void *stream);
 
+/* ------------------------------------------------------------- attention
+ * The other half of a layer, over a paged key/value cache: the "pre" graph of
+ * the engine article "93 token/s on one 8 GB card", section "Doorbell
+ * handshake", begins with attention and ends with the router.  The calls
+ * belong to a context (moe_attn_configure) and follow its conventions; they
+ * need no weights and no moe_configure.
+ *
+ * Cache: keys and values each [n_pages, n_kv, page_size, head_dim], caller-
+ * owned, 16-byte aligned, one pair per layer; bf16, or e4m3 with one fp32
+ * scale per KV head (stored value = x / scale; NULL = 1).  Position p of
+ * sequence b lives in page page_table[b, p / page_size], row p % page_size.
+ *
+ * A call brings the rows [row_off[b], row_off[b+1]) of each sequence b (none,
+ * one or many); kv_len[b] counts the sequence's tokens, these rows included,
+ * so row t of T sits at position kv_len[b] - T + t.  The tables are device
+ * data, read when the kernels run: a captured graph replays with whatever
+ * they hold then.  Rows from row_off[n_seqs] on belong to no sequence and are
+ * left as they were.  The device checks what it reads: a page id outside
+ * [0, n_pages), or offsets and lengths that contradict each other or the
+ * sizes given here, index nothing out of range, leave the rows concerned
+ * unwritten (or, for a page that is only read, unspecified), and set the
+ * device status (moe_sync returns DEVICE). */
+enum { MOE_KV_BF16 = 1, MOE_KV_E4M3 = 2 };
+
+typedef struct {
+  void *k, *v;                   /* the layer's cache */
+  const float *k_scale, *v_scale; /* fp32 [n_kv], positive, or NULL (e4m3 caches only) */
+  const int32_t *page_table;     /* [n_seqs, max_pages] */
+  const int32_t *row_off;        /* [n_seqs + 1], ascending, row_off[n_seqs] <= n_rows */
+  const int32_t *kv_len;         /* [n_seqs] */
+  int32_t n_pages, n_seqs, max_pages;
+  int32_t n_rows;                /* rows of q, k, v and out */
+} moe_kv_batch;
+
+/* RMSNorm of each query and key head: y = x (mean(x^2) + eps)^-1/2 gamma.
+ * Device fp32 [head_dim], 16-byte aligned; a NULL gamma is 1. */
+typedef struct {
+  const float *q_gamma, *k_gamma;
+  float eps;
+} moe_qk_norm;
+
+/* Rotary positions: the first rot_dim elements of a head form rot_dim / 2
+ * pairs, pair i turning by position * inv_freq[i] radians (device fp64
+ * [rot_dim / 2]; any frequency scaling is in the table).  Pairs are
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved.  rot_dim is a
+ * multiple of 8. */
+typedef struct {
+  const double *inv_freq;
+  int32_t rot_dim, interleaved;
+} moe_rope;
+
+/* moe_attn_configure: n_q query heads over n_kv key/value heads (n_q a
+ * multiple of n_kv) of head_dim elements, pages of page_size tokens (16, 32,
+ * 64, 128 or 256), cache_type MOE_KV_*.  Allocates the attention scratch;
+ * once per context, before or after moe_configure.  Errors: INVALID_ARG,
+ * NOT_SUPPORTED (head_dim other than 64 and 128), STATE (called before), OOM,
+ * CUDA. */
+MOE_API moe_status moe_attn_configure(moe_ctx *ctx, int n_q, int n_kv, int head_dim, int page_size,
+                                      int cache_type);
+
+/* moe_qk_norm_rope: q_out, k_out = the rows of q [n_rows, n_q, head_dim] and
+ * k [n_rows, n_kv, head_dim] normalised (norm NULL: not) and rotated to the
+ * positions pos int32 [n_rows] (rope NULL: not, and pos may be NULL); bf16,
+ * fp32 inside, one rounding.  Strides count elements between rows (the rows
+ * may be parts of a fused projection's), multiples of 4; rows 8-byte aligned.
+ * Outputs may be the inputs themselves (same pointer and stride), not
+ * otherwise overlap them.  Errors: INVALID_ARG, STATE. */
+MOE_API moe_status moe_qk_norm_rope(moe_ctx *ctx, int n_rows, const void *q, int64_t q_stride,
+                                    const void *k, int64_t k_stride, const int32_t *pos,
+                                    const moe_qk_norm *norm, const moe_rope *rope, void *q_out,
+                                    int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                                    void *stream);
+
+/* moe_kv_append: stores the call's keys (normalised and rotated as above, to
+ * their positions in the sequences) and values in the cache, and writes the
+ * queries, normalised and rotated, to q_out; q and q_out both NULL: keys and
+ * values only.  k, v: bf16 [n_rows, n_kv, head_dim], strided as above; q_out
+ * may be q itself.  Two sequences of a call must not share the pages that
+ * they append to.  Errors: INVALID_ARG, STATE, NOT_SUPPORTED (2^31 or more
+ * cache rows). */
+MOE_API moe_status moe_kv_append(moe_ctx *ctx, const moe_kv_batch *batch, const void *q,
+                                 int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                 int64_t v_stride, const moe_qk_norm *norm, const moe_rope *rope,
+                                 void *q_out, int64_t q_out_stride, void *stream);
+
+/* moe_attn_forward: attention of one decode or verify window per sequence,
+ * at most max_T <= 32 rows each, over the cache (which holds the window's own
+ * keys and values already):
+ *   out[i, h] = sum_j softmax_j(scale q[i, h].k[j, h']) v[j, h'],  h' = h / (n_q / n_kv),
+ * over the positions j <= i, with a window > 0 only those with i - j < window
+ * or j < n_sink (the first n_sink tokens stay visible).  q, out: bf16
+ * [n_rows, n_q, head_dim], 16-byte aligned, row strides in elements,
+ * multiples of 8; out may be q itself.  fp32 accumulation and softmax
+ * statistics; probabilities enter the product with the values in bf16 (fp16
+ * with an e4m3 cache).  Cache rows that no row of their sequence sees may
+ * hold anything; a NaN or infinite value that some row sees may reach the
+ * call's other rows of that sequence.  The cache's length is split over the
+ * GPU and joined within the launch; results do not depend on timing.
+ * Errors: INVALID_ARG, STATE, NOT_SUPPORTED (2^31 or more cache rows). */
+MOE_API moe_status moe_attn_forward(moe_ctx *ctx, const moe_kv_batch *batch, const void *q,
+                                    int64_t q_stride, int max_T, float scale, int window,
+                                    int n_sink, void *out, int64_t out_stride, void *stream);
+
+/* moe_attn_prefill: the same attention for prompt chunks: any number of rows
+ * per sequence, at most max_T.  Same arguments, results and errors. */
+MOE_API moe_status moe_attn_prefill(moe_ctx *ctx, const moe_kv_batch *batch, const void *q,
+                                    int64_t q_stride, int max_T, float scale, int window,
+                                    int n_sink, void *out, int64_t out_stride, void *stream);
+
 /* moe_sync: wait (polling cudaEventQuery, at most timeout_ms; < 0 = no
  * limit) until the work queued by this context has finished, then read and
  * clear the device error status.  Returns TIMEOUT, BAD_SLOT, DEVICE, CUDA or

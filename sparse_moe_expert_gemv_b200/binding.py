@@ -24,6 +24,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_OOM", 3: "MOE
  MOE_ERR_DEVICE, MOE_ERR_TIMEOUT, MOE_ERR_NOT_SUPPORTED) = range(1, 9)
 MOE_Q4_SYM_G32_F16 = 1
 MOE_Q2_ASYM_G64_F16 = 2
+MOE_KV_BF16, MOE_KV_E4M3 = 1, 2
 
 # every symbol include/moe.h declares
 EXPORTS = ("moe_create", "moe_configure", "moe_destroy", "moe_load_experts",
@@ -38,7 +39,8 @@ EXPORTS = ("moe_create", "moe_configure", "moe_destroy", "moe_load_experts",
            "moe_tier_prefetch", "moe_forward_tiered", "moe_tier_stats", "moe_tier_dump_trace",
            "moe_tier_sim_create", "moe_tier_sim_request", "moe_tier_sim_counts",
            "moe_tier_sim_destroy", "moe_rmsnorm", "moe_experts_given", "moe_ep_dispatch",
-           "moe_ep_combine", "moe_experts_rows")
+           "moe_ep_combine", "moe_experts_rows", "moe_attn_configure", "moe_qk_norm_rope",
+           "moe_kv_append", "moe_attn_forward", "moe_attn_prefill")
 
 
 class MoeError(RuntimeError):
@@ -55,12 +57,30 @@ class MoeStats(ctypes.Structure):
                 ("E", ctypes.c_int32), ("expert_count", ctypes.POINTER(ctypes.c_int32))]
 
 
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("row_off", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_rows", ctypes.c_int32)]
+
+
+class _QkNorm(ctypes.Structure):
+    _fields_ = [("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(SO_PATH):
         raise ImportError(f"{SO_PATH} is missing: build it with "
                           "`python -m sparse_moe_expert_gemv_b200.build`")
     L = ctypes.CDLL(SO_PATH)
     P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    I64 = ctypes.c_int64
     sig = {
         "moe_create": [I, I, I, I, I, ctypes.POINTER(P)],
         "moe_configure": [P, I, I, I, I],
@@ -101,6 +121,11 @@ def _load():
         "moe_ep_dispatch": [P, P, I, I, P, P, P, P, ctypes.POINTER(ctypes.c_int32), P],
         "moe_ep_combine": [P, I, P, P, P, P, P, P, P],
         "moe_experts_rows": [P, I, P, I, P, P, P],
+        "moe_attn_configure": [P, I, I, I, I, I],
+        "moe_qk_norm_rope": [P, I, P, I64, P, I64, P, P, P, P, I64, P, I64, P],
+        "moe_kv_append": [P, P, P, I64, P, I64, P, I64, P, P, P, I64, P],
+        "moe_attn_forward": [P, P, P, I64, I, F, I, I, P, I64, P],
+        "moe_attn_prefill": [P, P, P, I64, I, F, I, I, P, I64, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -176,6 +201,7 @@ def moe_configure(ctx, n_layers, n_shared, n_slots, max_tokens):
 
 
 def moe_destroy(ctx):
+    _attn.pop(ctx, None)
     _check(None, _lib.moe_destroy(ctx))
 
 
@@ -418,3 +444,164 @@ class TierSim:
 
     def __del__(self):
         self.close()
+
+
+# ------------------------------------------------------------- attention
+# Geometry and device of the contexts configured for attention: the calls
+# below take torch tensors and check their types, shapes, strides and device
+# against it, since the library sees addresses only.
+_attn = {}
+
+
+def moe_attn_configure(ctx, n_q, n_kv, head_dim, page_size, cache_type):
+    _check(ctx, _lib.moe_attn_configure(ctx, n_q, n_kv, head_dim, page_size, cache_type))
+    import torch
+    _attn[ctx] = (n_q, n_kv, head_dim, page_size, cache_type, torch.cuda.current_device())
+
+
+def _geometry(ctx):
+    g = _attn.get(ctx)
+    if g is None:
+        raise MoeError(MOE_ERR_STATE, "moe_attn_configure comes first")
+    return g
+
+
+def _dense(name, t, dtype, shape=None):
+    """A dense CUDA tensor of this type (and shape); its address."""
+    if not t.is_cuda or str(t.dtype) != "torch." + dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _head_rows(name, t, n, heads, dim, device):
+    """Rows [n, heads, dim] (or [n, heads * dim]) of 16-bit elements, dense
+    within a row: (address, elements between rows)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads == 1 or stride[1] == dim)
+    else:
+        ok = len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1
+    if not ok or shape[0] < n or t.element_size() != 2:
+        raise ValueError(f"{name}: bf16 rows [{n}, {heads}, {dim}], dense within a row, not {tuple(shape)}")
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name}: a tensor on the context's device (cuda:{device})")
+    # the stride of a single row means nothing
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * dim)
+
+
+class KvBatch:
+    """The rows of one call and the paged cache of one layer (moe_kv_batch).
+
+    k, v: [n_pages, n_kv, page_size, head_dim] bfloat16 or float8_e4m3fn (with
+    k_scale, v_scale: fp32 [n_kv] or None); page_table int32 [n_seqs,
+    max_pages], row_off int32 [n_seqs + 1], kv_len int32 [n_seqs].  Holds the
+    tensors; their contents are read when the calls run, so one batch object
+    serves every step whose tables are updated in place."""
+
+    def __init__(self, k, v, page_table, row_off, kv_len, n_rows, k_scale=None, v_scale=None):
+        e4m3 = str(k.dtype) == "torch.float8_e4m3fn"
+        kind = "float8_e4m3fn" if e4m3 else "bfloat16"
+        if k.dim() != 4:
+            raise ValueError("k: [n_pages, n_kv, page_size, head_dim]")
+        n_pages, n_kv = k.shape[0], k.shape[1]
+        if page_table.dim() != 2:
+            raise ValueError("page_table: [n_seqs, max_pages]")
+        n_seqs, max_pages = page_table.shape
+        tensors = [k, v, page_table, row_off, kv_len, k_scale, v_scale]
+        self.geometry = (n_kv, k.shape[3], k.shape[2], MOE_KV_E4M3 if e4m3 else MOE_KV_BF16)
+        self.c = _KvBatch(
+            _dense("k", k, kind), _dense("v", v, kind, k.shape),
+            None if k_scale is None else _dense("k_scale", k_scale, "float32", (n_kv,)),
+            None if v_scale is None else _dense("v_scale", v_scale, "float32", (n_kv,)),
+            _dense("page_table", page_table, "int32"), _dense("row_off", row_off, "int32", (n_seqs + 1,)),
+            _dense("kv_len", kv_len, "int32", (n_seqs,)), n_pages, n_seqs, max_pages, n_rows)
+        self.device = k.get_device()
+        if any(t is not None and t.get_device() != self.device for t in tensors):
+            raise ValueError("the batch's tensors are on different devices")
+        self.tensors = tensors
+        self.n_rows = n_rows
+        self.ref = ctypes.addressof(self.c)
+
+    def check(self, g):
+        if self.geometry != (g[1], g[2], g[3], g[4]) or self.device != g[5]:
+            raise ValueError(f"batch of (n_kv, head_dim, page_size, type) {self.geometry} on cuda:{self.device}: "
+                             f"the context has {g[1:5]} on cuda:{g[5]}")
+
+
+class QkNorm:
+    """RMSNorm of the query and key heads (moe_qk_norm): fp32 [head_dim] CUDA
+    tensors or None (= 1)."""
+
+    def __init__(self, q_gamma=None, k_gamma=None, eps=1e-6):
+        self.tensors = [t for t in (q_gamma, k_gamma) if t is not None]
+        self.c = _QkNorm(None if q_gamma is None else _dense("q_gamma", q_gamma, "float32"),
+                         None if k_gamma is None else _dense("k_gamma", k_gamma, "float32"), float(eps))
+        self.ref = ctypes.addressof(self.c)
+
+    def check(self, g):
+        if any(tuple(t.shape) != (g[2],) or t.get_device() != g[5] for t in self.tensors):
+            raise ValueError(f"norm weights: [{g[2]}] on cuda:{g[5]}")
+
+
+class Rope:
+    """Rotary positions (moe_rope): inv_freq float64 [rot_dim / 2] on the GPU,
+    radians per position."""
+
+    def __init__(self, inv_freq, rot_dim, interleaved=False):
+        self.tensors = [inv_freq]
+        self.c = _Rope(_dense("inv_freq", inv_freq, "float64", (rot_dim // 2,)), rot_dim, int(bool(interleaved)))
+        self.ref = ctypes.addressof(self.c)
+
+    def check(self, g):
+        if self.tensors[0].get_device() != g[5]:
+            raise ValueError(f"inv_freq: on cuda:{g[5]}")
+
+
+def _ref(handle, g):
+    if handle is None:
+        return None
+    handle.check(g)
+    return handle.ref
+
+
+def moe_qk_norm_rope(ctx, n_rows, q, k, pos, norm, rope, q_out, k_out, stream=None):
+    g = _geometry(ctx)
+    n_q, n_kv, dim, dev = g[0], g[1], g[2], g[5]
+    if pos is not None:
+        pp = _dense("pos", pos, "int32")
+        if pos.numel() < n_rows or pos.get_device() != dev:
+            raise ValueError(f"pos: int32 [{n_rows}] on cuda:{dev}")
+    else:
+        pp = None
+    _check(ctx, _lib.moe_qk_norm_rope(
+        ctx, n_rows, *_head_rows("q", q, n_rows, n_q, dim, dev), *_head_rows("k", k, n_rows, n_kv, dim, dev), pp,
+        _ref(norm, g), _ref(rope, g), *_head_rows("q_out", q_out, n_rows, n_q, dim, dev),
+        *_head_rows("k_out", k_out, n_rows, n_kv, dim, dev), _stream(stream)))
+
+
+def moe_kv_append(ctx, batch, q, k, v, norm, rope, q_out, stream=None):
+    """q and q_out may both be None (keys and values only)."""
+    g = _geometry(ctx)
+    n_q, n_kv, dim, dev, n = g[0], g[1], g[2], g[5], batch.n_rows
+    _check(ctx, _lib.moe_kv_append(
+        ctx, _ref(batch, g), *((None, 0) if q is None else _head_rows("q", q, n, n_q, dim, dev)),
+        *_head_rows("k", k, n, n_kv, dim, dev), *_head_rows("v", v, n, n_kv, dim, dev), _ref(norm, g),
+        _ref(rope, g), *((None, 0) if q_out is None else _head_rows("q_out", q_out, n, n_q, dim, dev)),
+        _stream(stream)))
+
+
+def _attend(fn, ctx, batch, q, max_T, scale, window, n_sink, out, stream):
+    g = _geometry(ctx)
+    n_q, dim, dev, n = g[0], g[2], g[5], batch.n_rows
+    _check(ctx, fn(ctx, _ref(batch, g), *_head_rows("q", q, n, n_q, dim, dev), max_T, scale, window, n_sink,
+                   *_head_rows("out", out, n, n_q, dim, dev), _stream(stream)))
+
+
+def moe_attn_forward(ctx, batch, q, max_T, scale, window, n_sink, out, stream=None):
+    _attend(_lib.moe_attn_forward, ctx, batch, q, max_T, scale, window, n_sink, out, stream)
+
+
+def moe_attn_prefill(ctx, batch, q, max_T, scale, window, n_sink, out, stream=None):
+    _attend(_lib.moe_attn_prefill, ctx, batch, q, max_T, scale, window, n_sink, out, stream)

@@ -1,0 +1,291 @@
+// kvcache.cuh -- query/key norms with the rotary positions, and the append
+// of new keys and values to the paged cache.
+//
+// A head row x of D elements becomes y = x (mean x^2 + eps)^-1/2 gamma (or
+// y = x without a norm), then each rotated pair (a, b) at frequency w and
+// position t becomes (a cos tw - b sin tw, b cos tw + a sin tw): all in fp32,
+// rounded once when stored.  The angle t w is formed and reduced to a
+// fraction of a turn in fp64: in fp32 a position of 10^6 would be off by up
+// to 0.06 rad.
+//
+// What bounds it: one read and one write of every row (plus launch latency
+// for a window's few rows).  A block takes `rows_per_block` rows, computes
+// their rotations once in shared memory for all heads, and streams the heads
+// with D / 8 lanes each, two 8-byte (four-element) pieces per lane placed so
+// that both elements of a pair sit in the same lane.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kKvThreads = 256;
+constexpr int kKvMaxRows = 4;   // rows per block
+constexpr int kKvMaxDim = 128;
+
+// A sequence's rows in the call and its cache length, checked: the offsets
+// and lengths are device data, and no index formed from them may leave the
+// caller's buffers.
+struct SeqView {
+  int row0, rows, kv;
+  bool ok;
+};
+
+MOE_HOST_DEV_INLINE SeqView seq_check(int row0, int end, int kv, int n_rows, int max_pages, int page) {
+  SeqView s;
+  s.row0 = row0;
+  s.kv = kv;
+  s.ok = row0 >= 0 && end >= row0 && end <= n_rows && kv >= end - row0 &&
+         (long long)kv <= (long long)max_pages * page;
+  s.rows = s.ok ? end - row0 : 0;
+  if (!s.ok) s.kv = 0;
+  return s;
+}
+MOE_DEV SeqView seq_view(const int *row_off, const int *kv_len, int b, int n_rows, int max_pages,
+                         int page) {
+  return seq_check(__ldg(row_off + b), __ldg(row_off + b + 1), __ldg(kv_len + b), n_rows, max_pages, page);
+}
+
+struct KvRowsParams {
+  const uint16_t *q, *k, *v;          // bf16 rows; v null without a cache
+  long long q_stride, k_stride, v_stride;  // elements between rows
+  uint16_t *q_out, *k_out;            // bf16; k_out null with a cache
+  long long q_out_stride, k_out_stride;
+  const int *pos;                     // [n_rows], without a cache
+  const float *q_gamma, *k_gamma;     // [D] or null
+  float eps;
+  int norm;
+  const double *inv_freq;             // [rot / 2] or null
+  int rot, interleaved;
+  int n_rows, n_q, n_kv, rows_per_block;
+  // cache
+  uint8_t *k_cache, *v_cache;         // [n_pages][n_kv][page][D]
+  const float *k_scale, *v_scale;     // e4m3: [n_kv] or null
+  const int *page_table, *row_off, *kv_len;
+  int n_pages, n_seqs, max_pages, page;
+  int *status;
+};
+
+MOE_DEV void bf16x4_to_float(uint2 u, float *x) {
+  x[0] = __uint_as_float(u.x << 16);
+  x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(u.y << 16);
+  x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+MOE_DEV uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+MOE_DEV uint2 float_to_bf16x4(const float *x) {
+  return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+}
+// Four e4m3 values, round to nearest even; finite values past the type's
+// largest (and infinities) become +-448, NaN stays NaN.
+MOE_DEV uint32_t float_to_e4m3x4(const float *x) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// CACHE 0: q and k rows to q_out and k_out; 1: q rows to q_out (when given),
+// k and v rows to a bf16 cache; 2: the same with an e4m3 cache.
+template <int D, int CACHE>
+__global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
+  constexpr int LPH = D / 8;  // lanes of a head row
+  constexpr int PRE = 3;      // head rows in flight per lane
+  __shared__ float2 s_cs[kKvMaxRows][kKvMaxDim / 2];
+  __shared__ int s_seq[kKvMaxRows];   // sequences that end at or before the row
+  __shared__ int s_pos[kKvMaxRows];
+  __shared__ long long s_at[kKvMaxRows];  // cache row of KV head 0, or -1
+  const int tid = threadIdx.x;
+  const int r0 = blockIdx.x * p.rows_per_block;
+  const int nr = min(p.rows_per_block, p.n_rows - r0);
+  if (tid < kKvMaxRows) s_seq[tid] = 0;
+  pdl_wait();
+
+  const int heads = p.n_q + p.n_kv * (CACHE ? 2 : 1);
+  const int hq0 = (CACHE && p.q == nullptr) ? p.n_q : 0;  // first head of the call
+  const int per_row = heads - hq0;
+  const int total = nr * per_row;
+  const int group = tid / LPH, sub = tid % LPH;
+  const uint32_t group_mask = ((1u << LPH) - 1u) << ((tid & 31) / LPH * LPH);  // the lanes of one head row
+  constexpr int NG = kKvThreads / LPH;
+  // the lane's two pieces of a head row: four first and four second elements
+  // of rotated pairs, or eight neighbours
+  int e0, e1;
+  const int half = p.rot / 2;
+  const bool turns = p.inv_freq != nullptr && 4 * sub < half;
+  if (turns && !p.interleaved) {
+    e0 = 4 * sub;
+    e1 = e0 + half;
+  } else {
+    e0 = 8 * sub;
+    e1 = e0 + 4;
+  }
+  auto load = [&](int item, uint2 &a, uint2 &b) {
+    const int r = item / per_row, h = hq0 + item - r * per_row;
+    const uint16_t *src;
+    const long long row = r0 + r;
+    if (h < p.n_q) src = p.q + row * p.q_stride + (long long)h * D;
+    else if (h < p.n_q + p.n_kv) src = p.k + row * p.k_stride + (long long)(h - p.n_q) * D;
+    else src = p.v + row * p.v_stride + (long long)(h - p.n_q - p.n_kv) * D;
+    a = *reinterpret_cast<const uint2 *>(src + e0);
+    b = *reinterpret_cast<const uint2 *>(src + e1);
+  };
+  // the first rows are on their way while the positions are looked up
+  uint2 xa[PRE], xb[PRE];
+#pragma unroll
+  for (int i = 0; i < PRE; ++i)
+    if (group + i * NG < total) load(group + i * NG, xa[i], xb[i]);
+
+  if (CACHE) {
+    // each row's sequence: the number of sequences that end at or before it
+    int cnt[kKvMaxRows] = {};
+    __syncthreads();
+    for (int b = tid; b < p.n_seqs; b += kKvThreads) {
+      const int end = __ldg(p.row_off + b + 1);
+#pragma unroll
+      for (int r = 0; r < kKvMaxRows; ++r) cnt[r] += end <= r0 + r;
+    }
+#pragma unroll
+    for (int r = 0; r < kKvMaxRows; ++r) {
+      const int c = __reduce_add_sync(0xffffffffu, cnt[r]);
+      if ((tid & 31) == 0 && c) atomicAdd(&s_seq[r], c);
+    }
+    __syncthreads();
+    if (tid < nr) {
+      const int row = r0 + tid, b = s_seq[tid];
+      int pos = -1;
+      long long at = -1;
+      if (b < p.n_seqs) {
+        const SeqView s = seq_view(p.row_off, p.kv_len, b, p.n_rows, p.max_pages, p.page);
+        if (!s.ok || row < s.row0 || row >= s.row0 + s.rows) {
+          atomicOr(p.status, kErrBadBatch);
+        } else {
+          pos = s.kv - s.rows + (row - s.row0);
+          const int pg = __ldg(p.page_table + (long long)b * p.max_pages + pos / p.page);
+          if ((unsigned)pg < (unsigned)p.n_pages)
+            at = (long long)pg * p.n_kv * p.page + pos % p.page;
+          else
+            atomicOr(p.status, kErrBadPage);
+        }
+      }
+      s_pos[tid] = pos;
+      s_at[tid] = at;
+    }
+  } else {
+    if (tid < nr) s_pos[tid] = p.pos ? __ldg(p.pos + r0 + tid) : 0;
+  }
+  __syncthreads();
+  if (p.inv_freq) {
+    for (int i = tid; i < nr * half; i += kKvThreads) {
+      const int r = i / half, j = i - r * half;
+      // the angle as a fraction of a turn, in [-1/2, 1/2]
+      const double t = (double)s_pos[r] * __ldg(p.inv_freq + j) * 0.15915494309189533577;
+      float s, c;
+      sincospif(2.f * (float)(t - rint(t)), &s, &c);
+      s_cs[r][j] = make_float2(c, s);
+    }
+    __syncthreads();
+  }
+
+  auto finish = [&](int item, uint2 a, uint2 b) {
+    const int r = item / per_row, h = hq0 + item - r * per_row;
+    const bool is_q = h < p.n_q, is_v = h >= p.n_q + p.n_kv;
+    float x[8];
+    bf16x4_to_float(a, x);
+    bf16x4_to_float(b, x + 4);
+    if (!is_v) {
+      if (p.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+#pragma unroll
+        for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
+        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+        const float *g = is_q ? p.q_gamma : p.k_gamma;
+        if (g) {
+          const float4 ga = __ldg(reinterpret_cast<const float4 *>(g + e0));
+          const float4 gb = __ldg(reinterpret_cast<const float4 *>(g + e1));
+          const float gg[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * gg[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= inv;
+        }
+      }
+      if (turns) {
+        const float2 *cs = &s_cs[r][4 * sub];
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 t = cs[i];
+            const float u = x[2 * i], w = x[2 * i + 1];
+            x[2 * i] = u * t.x - w * t.y;
+            x[2 * i + 1] = w * t.x + u * t.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 t = cs[i];
+            const float u = x[i], w = x[4 + i];
+            x[i] = u * t.x - w * t.y;
+            x[4 + i] = w * t.x + u * t.y;
+          }
+        }
+      }
+    }
+    const long long row = r0 + r;
+    if (is_q || !CACHE) {
+      if (CACHE && s_pos[r] < 0) return;  // a row of no sequence: left as it was
+      uint16_t *dst = is_q ? p.q_out + row * p.q_out_stride + (long long)h * D
+                           : p.k_out + row * p.k_out_stride + (long long)(h - p.n_q) * D;
+      *reinterpret_cast<uint2 *>(dst + e0) = float_to_bf16x4(x);
+      *reinterpret_cast<uint2 *>(dst + e1) = float_to_bf16x4(x + 4);
+      return;
+    }
+    if (!CACHE || s_at[r] < 0) return;
+    const int kh = is_v ? h - p.n_q - p.n_kv : h - p.n_q;
+    const long long at = (s_at[r] + (long long)kh * p.page) * D;
+    if (CACHE == 2) {
+      const float *scale = is_v ? p.v_scale : p.k_scale;
+      if (scale) {
+        const float s = __ldg(scale + kh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] / s;
+      }
+      uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + at;
+      *reinterpret_cast<uint32_t *>(dst + e0) = float_to_e4m3x4(x);
+      *reinterpret_cast<uint32_t *>(dst + e1) = float_to_e4m3x4(x + 4);
+    } else {
+      uint16_t *dst = reinterpret_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + at;
+      *reinterpret_cast<uint2 *>(dst + e0) = float_to_bf16x4(x);
+      *reinterpret_cast<uint2 *>(dst + e1) = float_to_bf16x4(x + 4);
+    }
+  };
+  // the next rows' loads go out before the present ones are finished
+  for (int base = 0; base < total; base += NG * PRE) {
+    uint2 ya[PRE], yb[PRE];
+#pragma unroll
+    for (int i = 0; i < PRE; ++i) {
+      ya[i] = xa[i];
+      yb[i] = xb[i];
+    }
+#pragma unroll
+    for (int i = 0; i < PRE; ++i) {
+      const int item = base + group + (PRE + i) * NG;
+      if (item < total) load(item, xa[i], xb[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < PRE; ++i) {
+      const int item = base + group + i * NG;
+      if (item < total) finish(item, ya[i], yb[i]);
+    }
+  }
+}
+
+}  // namespace moe

@@ -29,6 +29,7 @@
 #include "kernels.cuh"
 #include "prefill.cuh"
 #include "ep.cuh"
+#include "attn.cuh"
 #include "tier.h"
 
 using namespace moe;
@@ -117,6 +118,17 @@ struct moe_ctx {
   std::vector<cudaEvent_t> prof_ev;
   int prof_next = 0, prof_pending = 0;
   std::map<std::pair<void *, int>, cudaGraphExec_t> stack_graphs;
+  // attention (moe_attn_configure): geometry, and one allocation with the
+  // status word, the arrival counters and the parts of split rows
+  struct Attn {
+    bool ready = false;
+    int n_q = 0, n_kv = 0, dim = 0, page = 0, cache = 0;
+    int grid = 0;  // resident blocks of the attention kernel
+    uint8_t *mem = nullptr;
+    int *status = nullptr;
+    unsigned int *arrived = nullptr;
+    float *ws = nullptr;
+  } attn;
   std::string err;
 };
 
@@ -1398,6 +1410,7 @@ moe_status moe_destroy(moe_ctx *c) {
   dfree(c->d_bias);
   dfree(c->d_gamma);
   dfree(c->scratch);
+  dfree(c->attn.mem);
   if (c->trace) {
     unsigned long long *null_ptr = nullptr;
     cudaMemcpyToSymbol(g_trace, &null_ptr, sizeof null_ptr);
@@ -1920,7 +1933,7 @@ moe_status moe_ep_combine(moe_ctx *c, int N, const float *w, const void *y, cons
 
 moe_status moe_sync(moe_ctx *c, int timeout_ms) {
   if (!c) return MOE_ERR_INVALID_ARG;
-  if (!c->configured) return MOE_OK;
+  if (!c->configured && !c->attn.ready) return MOE_OK;
   // poll the stream of the most recent compute call, with a bound
   const auto t0 = std::chrono::steady_clock::now();
   for (;;) {
@@ -1932,9 +1945,15 @@ moe_status moe_sync(moe_ctx *c, int timeout_ms) {
       return fail(c, MOE_ERR_TIMEOUT, "moe_sync: not done after %d ms", timeout_ms);
     std::this_thread::sleep_for(std::chrono::microseconds(50));
   }
-  int st = 0;
-  CUDA_TRY(c, cudaMemcpyAsync(&st, c->status, sizeof(int), cudaMemcpyDeviceToHost, c->io));
-  CUDA_TRY(c, cudaMemsetAsync(c->status, 0, sizeof(int), c->io));
+  int st = 0, at = 0;
+  if (c->configured) {
+    CUDA_TRY(c, cudaMemcpyAsync(&st, c->status, sizeof(int), cudaMemcpyDeviceToHost, c->io));
+    CUDA_TRY(c, cudaMemsetAsync(c->status, 0, sizeof(int), c->io));
+  }
+  if (c->attn.ready) {
+    CUDA_TRY(c, cudaMemcpyAsync(&at, c->attn.status, sizeof(int), cudaMemcpyDeviceToHost, c->io));
+    CUDA_TRY(c, cudaMemsetAsync(c->attn.status, 0, sizeof(int), c->io));
+  }
   // a kernel that gave up a wait may have left a counter mid-count: start
   // the decode grid barrier, its hand-over flags and the fused-routing
   // ticket again from zero
@@ -1944,6 +1963,10 @@ moe_status moe_sync(moe_ctx *c, int timeout_ms) {
   }
   CUDA_TRY(c, cudaStreamSynchronize(c->io));
   if (st & kErrBadSlot) return fail(c, MOE_ERR_BAD_SLOT, "device status 0x%x: bad slot", st);
+  if (at & kErrBadPage) return fail(c, MOE_ERR_DEVICE, "device status 0x%x: a page id outside the cache", st | at);
+  if (at & kErrBadBatch)
+    return fail(c, MOE_ERR_DEVICE, "device status 0x%x: row offsets or lengths that contradict the batch", st | at);
+  st |= at;
   if (st) return fail(c, MOE_ERR_DEVICE, "device status 0x%x", st);
   return MOE_OK;
 }
@@ -2204,3 +2227,5 @@ moe_status moe_route_static_status(int *status_out, void *stream) {
 }
 
 }  // extern "C"
+
+#include "attn_api.cuh"
