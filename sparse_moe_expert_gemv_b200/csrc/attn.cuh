@@ -71,16 +71,16 @@ struct AttnParams {
 struct SeqTiles {
   int lead, first, n;
 };
-MOE_HOST_DEV_INLINE SeqTiles seq_tiles(const SeqView &s, int window, int n_sink) {
+MOE_HOST_DEV_INLINE SeqTiles seq_tiles(const SeqView &s, int window, int n_sink, int tile = kAtTile) {
   SeqTiles t{0, 0, 0};
   if (s.rows == 0) return t;
-  const int end = (s.kv - 1) / kAtTile + 1;
+  const int end = (s.kv - 1) / tile + 1;
   if (window > 0) {
     const long long lo = (long long)s.kv - s.rows - window + 1;  // first key the first row's window holds
     if (lo > 0) {
-      t.first = (int)(lo / kAtTile);
+      t.first = (int)(lo / tile);
       const long long sk = n_sink < lo ? n_sink : lo;
-      const int lead = (int)((sk + kAtTile - 1) / kAtTile);
+      const int lead = (int)((sk + tile - 1) / tile);
       t.lead = lead < t.first ? lead : t.first;
     }
   }

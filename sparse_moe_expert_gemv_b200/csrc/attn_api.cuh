@@ -136,8 +136,76 @@ cudaError_t launch_attn(moe_ctx *c, cudaStream_t s, const CUtensorMap &km, const
   return launch_attn_mt<D, FP8, 4>(c, s, km, vm, p);
 }
 
+// 3-D map of the query rows [n_rows][n_q][D]: boxes of 64 columns x `pack`
+// heads x 128 / pack rows, so a box is 128 tile rows.
+bool encode_q_map(CUtensorMap *map, const moe_ctx::Attn &a, const void *q, int n_rows, long long q_stride, int pack) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.dim, (cuuint64_t)a.n_q, (cuuint64_t)n_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.dim * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[3] = {64u, (cuuint32_t)pack, (cuuint32_t)(128 / pack)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_attn_prefill(cudaStream_t s, int grid, const CUtensorMap &qm, const CUtensorMap &km,
+                                const CUtensorMap &vm, const AttnPfParams &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kApThreads);
+  cfg.dynamicSmemBytes = AttnPfCfg<D>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, qm, km, vm, p);
+}
+
+// The tensor-core kernel over a bf16 cache.
+moe_status attend_chunk(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_stride, float scale, int window,
+                        int n_sink, void *out, int64_t out_stride, cudaStream_t s, const char *who) {
+  const moe_ctx::Attn &a = c->attn;
+  AttnPfParams p{};
+  p.out = (uint16_t *)out;
+  p.out_stride = out_stride;
+  p.page_table = b->page_table;
+  p.row_off = b->row_off;
+  p.kv_len = b->kv_len;
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.window = window;
+  p.n_sink = n_sink;
+  p.n_rows = b->n_rows;
+  p.n_q = a.n_q;
+  p.n_kv = a.n_kv;
+  p.group = a.n_q / a.n_kv;
+  while (p.pack_shift < 7 && p.group % (2 << p.pack_shift) == 0) ++p.pack_shift;
+  p.pack = 1 << p.pack_shift;
+  p.n_pages = b->n_pages;
+  p.n_seqs = b->n_seqs;
+  p.max_pages = b->max_pages;
+  p.page = a.page;
+  while ((1 << p.page_shift) < a.page) ++p.page_shift;
+  p.status = a.status;
+  CUtensorMap qm, km, vm;
+  const int box = a.page < kApTile ? a.page : kApTile;
+  if (!encode_q_map(&qm, a, q, b->n_rows, q_stride, p.pack) || !encode_cache_map(&km, a, b->k, b->n_pages, box) ||
+      !encode_cache_map(&vm, a, b->v, b->n_pages, box))
+    return fail(c, MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  // the row blocks of all sequences are at most this many (the rest leave at once)
+  const long long blocks = (long long)b->n_rows / (kApRows / p.pack) + b->n_seqs, grid = blocks * (a.n_q / p.pack);
+  if (grid > 0x7fffffffLL) return fail(c, MOE_ERR_NOT_SUPPORTED, "%s: %lld blocks", who, grid);
+  CUDA_TRY(c, a.dim == 128 ? launch_attn_prefill<128>(s, (int)grid, qm, km, vm, p)
+                           : launch_attn_prefill<64>(s, (int)grid, qm, km, vm, p));
+  return MOE_OK;
+}
+
 moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_stride, int max_T, float scale,
-                  int window, int n_sink, void *out, int64_t out_stride, void *stream, const char *who) {
+                  int window, int n_sink, void *out, int64_t out_stride, void *stream, bool chunk, const char *who) {
   moe_status st = attn_check(c, b, who);
   if (st != MOE_OK) return st;
   if (!b) return fail(c, MOE_ERR_INVALID_ARG, "%s: no batch", who);
@@ -149,6 +217,9 @@ moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_st
   if (b->n_rows == 0) return MOE_OK;
   if (!rows_ok(q, q_stride, width, 16) || !rows_ok(out, out_stride, width, 16))
     return fail(c, MOE_ERR_INVALID_ARG, "%s: q and out rows are 16-byte aligned, at least n_q * head_dim apart", who);
+  c->last_stream = (cudaStream_t)stream;
+  if (chunk && a.cache == MOE_KV_BF16 && (long long)max_T * (a.n_q / a.n_kv) > kAtMaxRows)
+    return attend_chunk(c, b, q, q_stride, scale, window, n_sink, out, out_stride, (cudaStream_t)stream, who);
   CUtensorMap km, vm;
   const int box = a.page < kAtTile ? a.page : kAtTile;
   if (!encode_cache_map(&km, a, b->k, b->n_pages, box) || !encode_cache_map(&vm, a, b->v, b->n_pages, box))
@@ -181,7 +252,6 @@ moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_st
   p.arrived = a.arrived;
   p.status = a.status;
   cudaStream_t s = (cudaStream_t)stream;
-  c->last_stream = s;
   const int rows = (int)std::min<long long>((long long)std::min(max_T, b->n_rows) * p.group, kAtMaxRows);
   const bool fp8 = a.cache == MOE_KV_E4M3;
   cudaError_t e;
@@ -216,6 +286,11 @@ moe_status moe_attn_configure(moe_ctx *c, int n_q, int n_kv, int head_dim, int p
   int blocks = kAtGridPerSm;
   cudaError_t e = head_dim == 128 ? (fp8 ? setup_attn_all<128, true>(&blocks) : setup_attn_all<128, false>(&blocks))
                                   : (fp8 ? setup_attn_all<64, true>(&blocks) : setup_attn_all<64, false>(&blocks));
+  if (e == cudaSuccess && !fp8)
+    e = head_dim == 128 ? cudaFuncSetAttribute(attn_prefill_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               AttnPfCfg<128>::SMEM)
+                        : cudaFuncSetAttribute(attn_prefill_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               AttnPfCfg<64>::SMEM);
   CUDA_TRY(c, e);
   if (blocks < 1) return fail(c, MOE_ERR_CUDA, "moe_attn_configure: the attention kernel does not fit this device");
   a.grid = c->n_sm * blocks;
@@ -313,13 +388,13 @@ moe_status moe_attn_forward(moe_ctx *c, const moe_kv_batch *b, const void *q, in
   if (max_T > kDecMaxT)
     return fail(c, MOE_ERR_INVALID_ARG, "moe_attn_forward: max_T=%d, at most %d (moe_attn_prefill takes chunks)", max_T,
                 kDecMaxT);
-  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, "moe_attn_forward");
+  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, false, "moe_attn_forward");
 }
 
 moe_status moe_attn_prefill(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_stride, int max_T,
                             float scale, int window, int n_sink, void *out, int64_t out_stride, void *stream) {
   if (!c) return MOE_ERR_INVALID_ARG;
-  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, "moe_attn_prefill");
+  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, true, "moe_attn_prefill");
 }
 
 }  // extern "C"

@@ -1,0 +1,450 @@
+// attn_prefill.cuh -- attention of prompt chunks over the paged cache on the
+// tensor cores (tcgen05).
+//
+// The mathematics is attn.cuh's.  A chunk has enough rows per KV head to fill
+// 128-row tiles, so here the two products are the work: 4 D flops a visible
+// (row, key) pair against one exponential.
+//
+// A block takes 256 rows: two 128-row tiles, each the rows of `pack` query
+// heads of one KV head (the largest power of two dividing the group) at 128 /
+// pack consecutive tokens, so few tokens of a tile lie above the diagonal.
+// Ten warps:
+//   8     TMA: the query tiles, then key and value tiles of 128 keys through
+//         a ring of slots (one box per page and 64 columns);
+//   9     issues the MMAs: S = Q K^T into tensor memory, O += P V with P read
+//         from tensor memory and V as it lies in the cache ([key][column]: an
+//         MN-major operand);
+//   0-3, 4-7  one thread per row of tile 0 and 1: reads its row of S, masks,
+//         keeps the running maximum and sum, and writes P (bf16) over S.
+// The two tiles alternate: while the tensor cores work for one, the other's
+// rows go through the exponentials.  O stays in tensor memory; it is rescaled
+// only when a row's maximum grew by more than 2^8 over the reference its
+// terms were scaled by (P then holds values up to 2^8, exact to bf16's step
+// like any other; sums are fp32).
+//
+// Tensor memory: S0, S1 (128 columns each, P over the first 64), O0, O1.
+#pragma once
+
+#include "attn.cuh"
+#include "prefill.cuh"
+
+namespace moe {
+
+constexpr int kApTile = 128;   // keys of a tile
+constexpr int kApRows = 256;   // rows of a block
+constexpr int kApThreads = 320;
+constexpr float kApSlack = 8.f;  // log2 of the growth that O is not rescaled for
+
+template <int D>
+struct AttnPfCfg {
+  static constexpr int HALVES = D / 64;                // 128-byte column boxes
+  static constexpr int BOX = kApTile * 128;            // 128 rows x 64 columns
+  static constexpr int TILE = HALVES * BOX;            // a query, key or value tile
+  static constexpr int SLOTS = D == 128 ? 5 : 8;
+  static constexpr int SMEM = 1024 + 2 * TILE + SLOTS * TILE;
+};
+
+struct AttnPfParams {
+  uint16_t *out;
+  long long out_stride;
+  const int *page_table, *row_off, *kv_len;
+  float scale_log2;
+  int window, n_sink;
+  int n_rows, n_q, n_kv, group, pack, pack_shift;
+  int n_pages, n_seqs, max_pages, page, page_shift;
+  int *status;
+};
+
+struct AttnPfShared {
+  unsigned long long q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], edge, drain;
+  long long scan[kApThreads / 32];
+  uint32_t tmem;
+  int item[2];  // sequence, row block
+  int dead;
+};
+static_assert(sizeof(AttnPfShared) <= 1024, "fits the block before the tiles");
+
+// Bounded wait that also ends when another warp of the block gave up.
+MOE_DEV bool mbar_wait_live(uint32_t bar, uint32_t parity, const int *dead) {
+  for (uint32_t i = 0; i < (1u << 20); ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<const volatile int *>(dead)) return false;
+  }
+  return false;
+}
+
+// Descriptor of an MN-major tile with 128-byte swizzle: lines of 64 columns,
+// one line per key; 8-key groups are 1024 B apart (stride offset), 64-column
+// halves BOX bytes (leading offset).
+MOE_DEV uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t half_bytes) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(half_bytes >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// D += A B with A (bf16 pairs) in tensor memory
+MOE_DEV void umma_f16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(db), "r"(idesc), "r"(accumulate));
+}
+MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+MOE_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+MOE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kApThreads, 1)
+    attn_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, const AttnPfParams p) {
+  using C = AttnPfCfg<D>;
+  extern __shared__ __align__(1024) unsigned char ap_smem[];
+  AttnPfShared &sh = *reinterpret_cast<AttnPfShared *>(ap_smem);
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const uint32_t q0 = smem_addr(ap_smem) + 1024, slot0 = q0 + 2 * C::TILE;
+  pdl_wait();
+
+  // ---- this block's item: head group fastest (blocks that share keys run
+  // together), then row blocks from the sequence's last (the longest) back
+  const int n_hg = p.n_q >> p.pack_shift;
+  const int hg = blockIdx.x % n_hg, item = blockIdx.x / n_hg;
+  const int tokens = kApRows >> p.pack_shift;  // of a block
+  const int per = (p.n_seqs + kApThreads - 1) / kApThreads;
+  const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
+  auto view = [&](int b) { return seq_view(p.row_off, p.kv_len, b, p.n_rows, p.max_pages, p.page); };
+  auto blocks_of = [&](const SeqView &s) { return (s.rows + tokens - 1) / tokens; };
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const SeqView s = view(b);
+    if (!s.ok && blockIdx.x == 0) atomicOr(p.status, kErrBadBatch);
+    mine += blocks_of(s);
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sh.scan[wid] = inc;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kApThreads / 32; ++w) {
+    if (w < wid) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  if (item >= total) return;  // block-uniform: the grid is sized for the most items there can be
+  inc += before;
+  if (item >= inc - mine && item < inc) {
+    long long at = inc - mine;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const int n = blocks_of(view(b));
+      if (item < at + n) {
+        sh.item[0] = b;
+        sh.item[1] = n - 1 - (int)(item - at);
+        break;
+      }
+      at += n;
+    }
+  }
+  if (tid == 0) {
+    mbar_init(smem_addr(&sh.q_full), 1);
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(smem_addr(&sh.kv_full[i]), 1);
+      mbar_init(smem_addr(&sh.kv_empty[i]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_addr(&sh.s_full[t]), 1);
+      mbar_init(smem_addr(&sh.p_full[t]), 4);
+      mbar_init(smem_addr(&sh.o_full[t]), 1);
+    }
+    mbar_init(smem_addr(&sh.edge), 1);
+    mbar_init(smem_addr(&sh.drain), 1);
+    sh.dead = 0;
+    fence_mbar_init();
+  }
+  if (wid == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int b = sh.item[0];
+  const SeqView s = view(b);
+  const int t_lo = sh.item[1] * tokens, t_hi = min(t_lo + tokens, s.rows);
+  const int pos0 = s.kv - s.rows;
+  const int kv_h = (hg << p.pack_shift) / p.group;
+  // the block's rows as a sequence of their own: its keys end with its last row
+  SeqView sv = s;
+  sv.rows = t_hi - t_lo;
+  sv.kv = pos0 + t_hi;
+  const SeqTiles tl = seq_tiles(sv, p.window, p.n_sink, kApTile);
+  auto give_up = [&]() {
+    *reinterpret_cast<volatile int *>(&sh.dead) = 1;
+    atomicOr(p.status, kErrTimeout);
+  };
+
+  if (wid == 8) {
+    // ---------------------------------------------------------- producer
+    const int pr = min(p.page, kApTile);
+    const int ppt = kApTile / pr;  // boxes along a tile's keys, at most 8
+    if (lane == 0) {
+      const uint32_t bar = smem_addr(&sh.q_full);
+      mbar_expect_tx(bar, 2 * C::TILE);
+      for (int t = 0; t < 2; ++t)
+        for (int h = 0; h < C::HALVES; ++h)
+          tma_load_3d(q0 + t * C::TILE + h * C::BOX, &qmap, h * 64, hg << p.pack_shift,
+                      s.row0 + t_lo + t * (tokens / 2), bar);
+    }
+    // keys that some row of the sequence sees: [0, sink_end) and [lo, kv)
+    const long long lo = p.window > 0 ? (long long)pos0 - p.window + 1 : 0;
+    const int sink_end = lo > 0 ? (int)min((long long)p.n_sink, lo) : 0;
+    const int my_page = lane / C::HALVES, my_half = lane % C::HALVES;
+    int issued = 0, edge_uses = 0;
+    bool ok = true;
+    for (int i = 0; i < 2 * tl.n && ok; ++i) {
+      const bool is_v = i & 1;
+      const int key0 = tile_at(tl, i >> 1) * kApTile;
+      const int st = i % C::SLOTS, use = i / C::SLOTS;
+      // the page of this lane's box: needed when it holds a key that is seen
+      const int first_key = key0 + my_page * pr;
+      const bool mine_needed = lane < ppt * C::HALVES && first_key < s.kv &&
+                               (first_key < sink_end || first_key + pr > lo);
+      int page = 0;
+      if (mine_needed) {
+        page = __ldg(p.page_table + (long long)b * p.max_pages + (first_key >> p.page_shift));
+        if ((unsigned)page >= (unsigned)p.n_pages) {
+          atomicOr(p.status, kErrBadPage);
+          page = 0;  // an in-bounds page; the call's result is reported as bad
+        }
+      }
+      const int boxes = __popc(__ballot_sync(0xffffffffu, mine_needed));
+      // values no row of the sequence sees may hold anything: such rows of the
+      // tile become zeros before the tensor cores read them
+      const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < lo && key0 + kApTile > sink_end));
+      if (use > 0) ok = mbar_wait_live(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t full = smem_addr(&sh.kv_full[st]), bar = edge ? smem_addr(&sh.edge) : full;
+      const uint32_t dst = slot0 + st * C::TILE;
+      if (lane == 0) mbar_expect_tx(bar, (uint32_t)boxes * pr * 128);
+      __syncwarp();
+      if (mine_needed)
+        tma_load_2d(dst + my_half * C::BOX + my_page * pr * 128, is_v ? &vmap : &kmap, my_half * 64,
+                    (page * p.n_kv + kv_h) * p.page + (first_key & (p.page - 1)), bar);
+      ++issued;
+      if (edge) {
+        ok = mbar_wait_bounded(bar, edge_uses & 1);
+        ++edge_uses;
+        for (int r = 0; r < kApTile; ++r) {
+          const int j = key0 + r;
+          if (j < s.kv && (j < sink_end || j >= lo)) continue;
+          // a key's line in each half: 8 16-byte pieces
+          if (lane < 8 * C::HALVES)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (lane >> 3) * C::BOX + r * 128 +
+                                                                       (lane & 7) * 16),
+                         "r"(0)
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) mbar_arrive(full);
+      }
+    }
+    if (!ok && lane == 0) give_up();
+    // no tile may land after the block has gone
+    (void)mbar_wait_bounded(smem_addr(&sh.q_full), 0);
+    for (int i = max(0, issued - C::SLOTS); i < issued; ++i)
+      (void)mbar_wait_bounded(smem_addr(&sh.kv_full[i % C::SLOTS]), (i / C::SLOTS) & 1);
+  } else if (wid == 9) {
+    // -------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kApTile);
+      constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
+      bool ok = mbar_wait_live(smem_addr(&sh.q_full), 0, &sh.dead);
+      auto kv_wait = [&](int i) {
+        return mbar_wait_live(smem_addr(&sh.kv_full[i % C::SLOTS]), (i / C::SLOTS) & 1, &sh.dead);
+      };
+      auto scores = [&](int t, int i) {  // S_t = Q_t K^T, the key tile in slot i
+        const uint32_t qa = q0 + t * C::TILE, ka = slot0 + (i % C::SLOTS) * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::BOX + (kk & 3) * 32;
+          umma_f16(tmem + t * 128, umma_desc_sw128(qa + off), umma_desc_sw128(ka + off), IDESC_S, kk != 0);
+        }
+        umma_commit(smem_addr(&sh.s_full[t]));
+      };
+      auto values = [&](int t, int i, bool first) {  // O_t += P_t V
+        const uint32_t va = slot0 + (i % C::SLOTS) * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < kApTile / 16; ++kk)
+          umma_f16_ta(tmem + 256 + t * D, tmem + t * 128 + kk * 8, umma_desc_mn_sw128(va + kk * 2048, C::BOX),
+                      IDESC_O, !(first && kk == 0));
+      };
+      ok = ok && kv_wait(0);
+      if (ok) {
+        tc_fence_after();
+        scores(0, 0);
+        scores(1, 0);
+        umma_commit(smem_addr(&sh.kv_empty[0]));
+      }
+      for (int j = 0; j < tl.n && ok; ++j) {
+        const int vi = 2 * j + 1, kn = 2 * j + 2;
+        const bool more = j + 1 < tl.n;
+        ok = kv_wait(vi) && (!more || kv_wait(kn));
+        for (int t = 0; t < 2 && ok; ++t) {
+          ok = mbar_wait_live(smem_addr(&sh.p_full[t]), j & 1, &sh.dead);
+          if (!ok) break;
+          tc_fence_after();
+          values(t, vi, j == 0);
+          if (t == 1) umma_commit(smem_addr(&sh.kv_empty[vi % C::SLOTS]));
+          // in order behind the product that reads P, whose columns it overwrites
+          if (more) scores(t, kn);
+          else umma_commit(smem_addr(&sh.o_full[t]));
+        }
+        if (more && ok) umma_commit(smem_addr(&sh.kv_empty[kn % C::SLOTS]));
+      }
+      if (!ok) {
+        give_up();
+        // every issued MMA is complete before tensor memory is released
+        umma_commit(smem_addr(&sh.drain));
+        (void)mbar_wait_bounded(smem_addr(&sh.drain), 0);
+      }
+    }
+  } else {
+    // -------------------------------------------------- one thread per row
+    const int t = wid >> 2, row = (wid & 3) * 32 + lane;
+    const int tok = t_lo + t * (tokens / 2) + (row >> p.pack_shift);
+    const int head = (hg << p.pack_shift) + (row & (p.pack - 1));
+    const bool mine_ok = tok < t_hi;
+    const int pos = pos0 + min(tok, t_hi - 1);
+    const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * D;
+    float m_ref = -INFINITY, l_run = 0.f;  // m_ref in units of the scores times scale_log2
+    bool ok = true;
+    for (int j = 0; j < tl.n; ++j) {
+      ok = mbar_wait_live(smem_addr(&sh.s_full[t]), j & 1, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_at + c * 32, r[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_wait(r[c]);
+      const int key0 = tile_at(tl, j) * kApTile;
+      // columns [0, hi] by position; with a window from lo on, or below sk
+      const int hi = pos - key0;
+      const long long lo = p.window > 0 ? (long long)pos - p.window + 1 - key0 : 0;
+      const int sk = p.n_sink - key0;
+      const bool whole = hi >= kApTile - 1 && (lo <= 0 || sk >= kApTile);
+      if (__any_sync(0xffffffffu, !whole)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int col = c * 32 + e;
+            if (!(col <= hi && (col >= lo || col < sk))) r[c][e] = 0xff800000u;  // -inf
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          mx = fmaxf(mx, fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
+      mx *= p.scale_log2;
+      // the reference follows the maximum when it fell 2^kApSlack behind (the
+      // commit that brought S also says that O holds every earlier product)
+      const bool first = m_ref == -INFINITY;
+      const bool grow = mx > m_ref + kApSlack;
+      float corr = 1.f;
+      if (first) {
+        m_ref = mx;
+      } else if (grow) {
+        corr = ex2(m_ref - mx);
+        m_ref = mx;
+      }
+      if (__any_sync(0xffffffffu, corr != 1.f)) {
+        l_run *= corr;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32_issue(o_at + c * 32, o);
+          tmem_ld32_wait(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+          tmem_st32(o_at + c * 32, o);
+        }
+      }
+      const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: 2^-inf = 0
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int cc = c + (e >> 4), k = (e & 15) * 2;
+          const float p0 = ex2(__fmaf_rn(__uint_as_float(r[cc][k]), p.scale_log2, neg));
+          const float p1 = ex2(__fmaf_rn(__uint_as_float(r[cc][k + 1]), p.scale_log2, neg));
+          sum0 += p0;
+          sum1 += p1;
+          w[e] = pack_bf16(p0, p1);
+        }
+        tmem_st32(s_at + c * 16, w);
+      }
+      l_run += sum0 + sum1;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[t]));
+    }
+    if (ok) ok = mbar_wait_live(smem_addr(&sh.o_full[t]), 0, &sh.dead);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+      uint16_t *dst = p.out + (long long)(s.row0 + tok) * p.out_stride + (long long)head * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32_issue(o_at + c * 32, o);
+        tmem_ld32_wait(o);
+        if (mine_ok) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 v;
+            v.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+            v.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            v.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+            v.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+            *reinterpret_cast<uint4 *>(dst + c * 32 + e) = v;
+          }
+        }
+      }
+    } else if (lane == 0) {
+      give_up();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (wid == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+}  // namespace moe

@@ -30,6 +30,7 @@
 #include "prefill.cuh"
 #include "ep.cuh"
 #include "attn.cuh"
+#include "attn_prefill.cuh"
 #include "tier.h"
 
 using namespace moe;

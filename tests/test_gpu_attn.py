@@ -371,3 +371,51 @@ def test_refusals(B, make_ctx):
     with pytest.raises(ValueError):
         B.moe_attn_forward(ctx, other, q, 2, 0.1, 0, 0, out)
     B.moe_sync(ctx, 60000)
+
+
+# ------------------------------------------------------------------ chunks
+CHUNKS = [
+    # rows, kv, page, n_q, n_kv, dim, window, sinks
+    ([128], [128], 64, 16, 2, 128, 0, 0),
+    ([65], [65], 16, 4, 4, 128, 0, 0),              # one head per tile
+    ([33, 0, 100, 1], [33, 9, 357, 40], 32, 16, 4, 128, 0, 0),
+    ([257, 300], [257, 1111], 128, 12, 4, 64, 0, 0),  # three heads a group
+    ([1000], [3000], 256, 24, 4, 128, 0, 0),
+    ([777, 5], [777, 130], 16, 10, 2, 64, 0, 0),
+    ([300], [2000], 64, 28, 4, 128, 200, 4),
+    ([513, 90], [1500, 90], 16, 8, 1, 64, 64, 0),
+    ([200], [900], 32, 32, 2, 128, 1, 1),
+    ([150], [150], 64, 8, 8, 64, 100000, 3),
+    ([400, 400], [5000, 640], 64, 20, 4, 128, 130, 200),
+    ([40], [10], 16, 16, 16, 64, 0, 0),             # replaced below by kv = rows
+    ([2100], [2100], 64, 16, 4, 128, 1024, 70),
+    ([70] * 20, [70 + 31 * i for i in range(20)], 32, 8, 2, 128, 0, 0),
+]
+CHUNKS = [(r, [max(a, b) for a, b in zip(r, k)], *rest) for r, k, *rest in CHUNKS]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows,kv,page,n_q,n_kv,dim,window,sinks", CHUNKS)
+def test_prefill(B, make_ctx, e4m3, rows, kv, page, n_q, n_kv, dim, window, sinks):
+    run_attention(B, make_ctx, B.moe_attn_prefill, e4m3, rows, kv, page, n_q, n_kv, dim, window, sinks)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", [2, 300])
+def test_scores_that_keep_growing(B, make_ctx, e4m3, rows):
+    """Later keys score higher and higher, so the running maximum moves in
+    every tile; and the reverse, where the first keys hold everything."""
+    ctx = make_ctx(8, 2, 128, 64, e4m3)
+    for sign in (1.0, -1.0):
+        cache = A.Cache([1500], 2, 128, 64, e4m3, seed=3)
+        for i, p in enumerate(cache.pages[0]):
+            ramp = (torch.arange(64, device="cuda") + 64 * i).float()[:, None] * (0.02 if not e4m3 else 0.2) * sign
+            cache.k[p] = (cache.k[p].float() * 0.25 + ramp).to(cache.k.dtype)
+        q = rnd((rows, 8, 128), 4).abs()
+        out = torch.empty_like(q)
+        fn = B.moe_attn_forward if rows <= 32 else B.moe_attn_prefill
+        fn(ctx, cache.batch(B, [rows]), q, rows, 1 / math.sqrt(128), 0, 0, out)
+        cache.kv = [1500]
+        want, tol = A.attention64(q, cache, [rows], 1 / math.sqrt(128), 0, 0)
+        close(out, want, tol)
+    B.moe_sync(ctx, 60000)
