@@ -87,6 +87,14 @@ MOE_HOST_DEV_INLINE SeqTiles seq_tiles(const SeqView &s, int window, int n_sink,
   t.n = t.lead + end - t.first;
   return t;
 }
+// Whether some row of the sequence sees one of the n keys from `key` on (the
+// rows together see [0, min(n_sink, lo)) and [lo, kv), lo the first row's
+// window).
+MOE_HOST_DEV_INLINE bool keys_seen(const SeqView &s, int window, int n_sink, int key, int n) {
+  if (key >= s.kv) return false;
+  const long long lo = window > 0 ? (long long)s.kv - s.rows - window + 1 : 0;
+  return (long long)key + n > lo || key < n_sink;
+}
 MOE_HOST_DEV_INLINE int tile_at(const SeqTiles &t, int k) { return k < t.lead ? k : k - t.lead + t.first; }
 // Units of a block's run: equal runs over the grid, none shorter than min_units.
 MOE_HOST_DEV_INLINE long long run_length(long long total, long long grid, long long min_units) {
@@ -283,10 +291,6 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         held_at = pg0;
         const int i = pg0 + lane;
         held = i < n_pg ? __ldg(p.page_table + (long long)c.b * p.max_pages + i) : 0;
-        if ((unsigned)held >= (unsigned)p.n_pages) {
-          atomicOr(p.status, kErrBadPage);
-          held = 0;  // an in-bounds page; the call's result is reported as bad
-        }
       }
       const int st = (int)(issued % S);
       const uint32_t use = (uint32_t)(issued / S);
@@ -297,11 +301,19 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         if (lane == 0) give_up();
         break;
       }
-      const int have = min(ppt, n_pg - pg0);  // boxes whose page holds keys
-      const int page = __shfl_sync(0xffffffffu, held, min(pg0 - held_at + my_page, 31));
-      if (lane == 0) mbar_expect_tx(bar, (uint32_t)have * pr * C::ROWB * 2);
+      // a box is loaded when its page holds a key that some row sees; the
+      // entries of other pages (given back, or never there) are not looked at
+      int page = __shfl_sync(0xffffffffu, held, min(pg0 - held_at + my_page, 31));
+      const int first_key = key0 + my_page * pr;
+      const bool need = lane < boxes && keys_seen(c.s, p.window, p.n_sink, first_key, pr);
+      if (need && (unsigned)page >= (unsigned)p.n_pages) {
+        atomicOr(p.status, kErrBadPage);
+        page = 0;  // an in-bounds page; the call's result is reported as bad
+      }
+      const int n_box = __popc(__ballot_sync(0xffffffffu, need));
+      if (lane == 0) mbar_expect_tx(bar, (uint32_t)n_box * pr * C::LINE);
       __syncwarp();
-      if (lane < boxes && my_page < have) {
+      if (need) {
         const uint32_t dst = stage0 + (uint32_t)(st * 2 + my_v) * C::TILE +
                              (uint32_t)my_col * (kAtTile * C::LINE) + (uint32_t)my_page * pr * C::LINE;
         const int y = (page * p.n_kv + blk_h) * p.page + (key0 & (p.page - 1));

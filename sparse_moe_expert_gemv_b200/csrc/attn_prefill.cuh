@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
       const int st = i % C::SLOTS, use = i / C::SLOTS;
       // the page of this lane's box: needed when it holds a key that is seen
       const int first_key = key0 + my_page * pr;
-      const bool mine_needed = lane < ppt * C::HALVES && first_key < s.kv &&
-                               (first_key < sink_end || first_key + pr > lo);
+      const bool mine_needed =
+          lane < ppt * C::HALVES && keys_seen(s, p.window, p.n_sink, first_key, pr);
       int page = 0;
       if (mine_needed) {
         page = __ldg(p.page_table + (long long)b * p.max_pages + (first_key >> p.page_shift));

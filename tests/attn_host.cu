@@ -45,6 +45,12 @@ static void tiles() {
               seen = j <= i && (w <= 0 || i - j < w || j < sk);
             if (seen) want.insert(j / kAtTile);
           }
+          for (int j = 0; j < kv + 70; j += 16) {  // a page is needed when one of its keys is seen
+            bool seen = false;
+            for (int x = j; x < j + 16 && x < kv && !seen; ++x)
+              for (int i = kv - rows; i < kv && !seen; ++i) seen = x <= i && (w <= 0 || i - x < w || x < sk);
+            CHECK(seen == keys_seen(s, w, sk, j, 16));
+          }
           for (int x : want) CHECK(got.count(x));
           CHECK(got.size() <= want.size() + 1);
         }

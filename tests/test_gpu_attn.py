@@ -199,6 +199,11 @@ def run_attention(B, make_ctx, fn, e4m3, rows, kv, page, n_q, n_kv, dim, window,
                 for t, x in ((cache.k, float("inf")), (cache.v, float("nan"))):
                     A.as_bytes(t)[cache.pages[b][j // page], :, j % page] = A.as_bytes(
                         torch.tensor(x, device="cuda").to(t.dtype))
+        # and pages that hold no visible key are given back
+        for b, (r, length) in enumerate(zip(rows, kv)):
+            for i in range(len(cache.pages[b])):
+                if r and i * page >= sinks and (i + 1) * page <= length - r - window + 1:
+                    cache.table[b, i] = -1 - i
     wide = rnd((n + extra, n_q + 3, dim), 12, scale=2.0)
     q = wide[:, 1:n_q + 1]
     scale = scale or 1 / math.sqrt(dim)
