@@ -32,7 +32,8 @@ namespace moe {
 
 constexpr int kApTile = 128;   // keys of a tile
 constexpr int kApRows = 256;   // rows of a block
-constexpr int kApThreads = 320;
+constexpr int kApThreads = 384;  // warps 10 and 11 only give up registers
+constexpr int kApPoly = 1;      // of four pairs of exponentials, those on the FMA units
 constexpr float kApSlack = 8.f;  // log2 of the growth that O is not rescaled for
 
 template <int D>
@@ -56,7 +57,7 @@ struct AttnPfParams {
 };
 
 struct AttnPfShared {
-  unsigned long long q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], edge, drain;
+  unsigned long long q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2][2], o_full[2], edge, drain;
   long long scan[kApThreads / 32];
   uint32_t tmem;
   int item[2];  // sequence, row block
@@ -97,6 +98,14 @@ MOE_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
       "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
+MOE_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
 MOE_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 MOE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -104,6 +113,73 @@ MOE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int
       "[%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+// Two fp32 values in one register pair: one instruction for both.
+MOE_DEV uint64_t f2_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MOE_DEV void f2_unpack(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+MOE_DEV uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x of both on the FMA units: x = n + f with |f| <= 1/2 (n by adding and
+// taking away 1.5 2^23), 2^f by the degree-4 polynomial whose largest relative
+// error on that interval is least (2.6e-6, a least-squares fit reweighted by
+// its own error), n added to the exponent.  x below -126 counts as -126.
+MOE_DEV uint64_t f2_exp2(uint64_t x) {
+  constexpr float kRound = 12582912.f;
+  float a, b;
+  f2_unpack(x, a, b);
+  x = f2_pack(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const uint64_t t = f2_add(x, f2_pack(kRound, kRound));
+  const uint64_t n = f2_add(t, f2_pack(-kRound, -kRound));
+  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), x);
+  uint64_t y = f2_fma(f2_pack(0.00957006868f, 0.00957006868f), f, f2_pack(0.0559178069f, 0.0559178069f));
+  y = f2_fma(y, f, f2_pack(0.240247443f, 0.240247443f));
+  y = f2_fma(y, f, f2_pack(0.69312185f, 0.69312185f));
+  y = f2_fma(y, f, f2_pack(0.999999285f, 0.999999285f));
+  float t0, t1, y0, y1;
+  f2_unpack(t, t0, t1);
+  f2_unpack(y, y0, y1);
+  y0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23));
+  y1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23));
+  return f2_pack(y0, y1);
+}
+
+// P of 64 columns (two loads' registers) of a row: p = 2^(s scale + neg), the
+// bf16 pairs in w and the sum of both halves added to `sum`.  Of every four
+// pairs POLY go to the FMA units, the others to the special function unit,
+// which alone would take as long as the products.
+template <int POLY>
+MOE_DEV void row_exp2(const uint32_t (&r)[32], uint64_t scale, uint64_t neg, uint32_t (&w)[16], uint64_t &sum) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), scale, neg);
+    float p0, p1;
+    if ((e & 3) >= 4 - POLY) {
+      const uint64_t y = f2_exp2(x);
+      sum = f2_add(sum, y);
+      f2_unpack(y, p0, p1);
+    } else {
+      f2_unpack(x, p0, p1);
+      p0 = ex2(p0);
+      p1 = ex2(p1);
+      sum = f2_add(sum, f2_pack(p0, p1));
+    }
+    w[e] = pack_bf16(p0, p1);
+  }
 }
 
 template <int D>
@@ -167,7 +243,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_addr(&sh.s_full[t]), 1);
-      mbar_init(smem_addr(&sh.p_full[t]), 4);
+      mbar_init(smem_addr(&sh.p_full[t][0]), 4);
+      mbar_init(smem_addr(&sh.p_full[t][1]), 4);
       mbar_init(smem_addr(&sh.o_full[t]), 1);
     }
     mbar_init(smem_addr(&sh.edge), 1);
@@ -199,8 +276,12 @@ __global__ void __launch_bounds__(kApThreads, 1)
     atomicOr(p.status, kErrTimeout);
   };
 
+  // 168 registers a thread at launch (384 threads): the rows' warps take 216
+  // of the last four's share: 256 * 216 + 128 * 72 = 384 * 168
+  auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); };
   if (wid == 8) {
     // ---------------------------------------------------------- producer
+    few_registers();
     const int pr = min(p.page, kApTile);
     const int ppt = kApTile / pr;  // boxes along a tile's keys, at most 8
     if (lane == 0) {
@@ -215,55 +296,57 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const long long lo = p.window > 0 ? (long long)pos0 - p.window + 1 : 0;
     const int sink_end = lo > 0 ? (int)min((long long)p.n_sink, lo) : 0;
     const int my_page = lane / C::HALVES, my_half = lane % C::HALVES;
+    // the page of this lane's box in tile j, or -1 when no row sees a key of it
+    auto page_of = [&](int j) {
+      const int first_key = tile_at(tl, j) * kApTile + my_page * pr;
+      if (lane >= ppt * C::HALVES || !keys_seen(s, p.window, p.n_sink, first_key, pr)) return -1;
+      int page = __ldg(p.page_table + (long long)b * p.max_pages + (first_key >> p.page_shift));
+      if ((unsigned)page >= (unsigned)p.n_pages) {
+        atomicOr(p.status, kErrBadPage);
+        page = 0;  // an in-bounds page; the call's result is reported as bad
+      }
+      return page;
+    };
     int issued = 0, edge_uses = 0;
     bool ok = true;
-    for (int i = 0; i < 2 * tl.n && ok; ++i) {
-      const bool is_v = i & 1;
-      const int key0 = tile_at(tl, i >> 1) * kApTile;
-      const int st = i % C::SLOTS, use = i / C::SLOTS;
-      // the page of this lane's box: needed when it holds a key that is seen
-      const int first_key = key0 + my_page * pr;
-      const bool mine_needed =
-          lane < ppt * C::HALVES && keys_seen(s, p.window, p.n_sink, first_key, pr);
-      int page = 0;
-      if (mine_needed) {
-        page = __ldg(p.page_table + (long long)b * p.max_pages + (first_key >> p.page_shift));
-        if ((unsigned)page >= (unsigned)p.n_pages) {
-          atomicOr(p.status, kErrBadPage);
-          page = 0;  // an in-bounds page; the call's result is reported as bad
-        }
-      }
-      const int boxes = __popc(__ballot_sync(0xffffffffu, mine_needed));
-      // values no row of the sequence sees may hold anything: such rows of the
-      // tile become zeros before the tensor cores read them
-      const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < lo && key0 + kApTile > sink_end));
-      if (use > 0) ok = mbar_wait_live(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t full = smem_addr(&sh.kv_full[st]), bar = edge ? smem_addr(&sh.edge) : full;
-      const uint32_t dst = slot0 + st * C::TILE;
-      if (lane == 0) mbar_expect_tx(bar, (uint32_t)boxes * pr * 128);
-      __syncwarp();
-      if (mine_needed)
-        tma_load_2d(dst + my_half * C::BOX + my_page * pr * 128, is_v ? &vmap : &kmap, my_half * 64,
-                    (page * p.n_kv + kv_h) * p.page + (first_key & (p.page - 1)), bar);
-      ++issued;
-      if (edge) {
-        ok = mbar_wait_bounded(bar, edge_uses & 1);
-        ++edge_uses;
-        for (int r = 0; r < kApTile; ++r) {
-          const int j = key0 + r;
-          if (j < s.kv && (j < sink_end || j >= lo)) continue;
-          // a key's line in each half: 8 16-byte pieces
-          if (lane < 8 * C::HALVES)
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (lane >> 3) * C::BOX + r * 128 +
-                                                                       (lane & 7) * 16),
-                         "r"(0)
-                         : "memory");
-        }
-        fence_proxy_async_smem();
+    int next = page_of(0);
+    for (int j = 0; j < tl.n && ok; ++j) {
+      const int page = next;
+      if (j + 1 < tl.n) next = page_of(j + 1);  // on its way while this tile's slots come free
+      const int key0 = tile_at(tl, j) * kApTile;
+      const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+      const int y = (page * p.n_kv + kv_h) * p.page + ((key0 + my_page * pr) & (p.page - 1));
+      for (int is_v = 0; is_v < 2 && ok; ++is_v, ++issued) {
+        const int st = issued % C::SLOTS, use = issued / C::SLOTS;
+        // values no row of the sequence sees may hold anything: such rows of
+        // the tile become zeros before the tensor cores read them
+        const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < lo && key0 + kApTile > sink_end));
+        if (use > 0) ok = mbar_wait_live(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
         ok = __all_sync(0xffffffffu, ok);
-        if (lane == 0) mbar_arrive(full);
+        if (!ok) break;
+        const uint32_t full = smem_addr(&sh.kv_full[st]), bar = edge ? smem_addr(&sh.edge) : full;
+        const uint32_t dst = slot0 + st * C::TILE;
+        if (lane == 0) mbar_expect_tx(bar, (uint32_t)boxes * pr * 128);
+        __syncwarp();
+        if (page >= 0)
+          tma_load_2d(dst + my_half * C::BOX + my_page * pr * 128, is_v ? &vmap : &kmap, my_half * 64, y, bar);
+        if (edge) {
+          ok = mbar_wait_bounded(bar, edge_uses & 1);
+          ++edge_uses;
+          for (int r = 0; r < kApTile; ++r) {
+            const int k = key0 + r;
+            if (k < s.kv && (k < sink_end || k >= lo)) continue;
+            // a key's line in each half: 8 16-byte pieces
+            if (lane < 8 * C::HALVES)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (lane >> 3) * C::BOX + r * 128 +
+                                                                         (lane & 7) * 16),
+                           "r"(0)
+                           : "memory");
+          }
+          fence_proxy_async_smem();
+          ok = __all_sync(0xffffffffu, ok);
+          if (lane == 0) mbar_arrive(full);
+        }
       }
     }
     if (!ok && lane == 0) give_up();
@@ -273,6 +356,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
       (void)mbar_wait_bounded(smem_addr(&sh.kv_full[i % C::SLOTS]), (i / C::SLOTS) & 1);
   } else if (wid == 9) {
     // -------------------------------------------------------- MMA issuer
+    few_registers();
     if (lane == 0) {
       constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kApTile);
       constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
@@ -289,10 +373,10 @@ __global__ void __launch_bounds__(kApThreads, 1)
         }
         umma_commit(smem_addr(&sh.s_full[t]));
       };
-      auto values = [&](int t, int i, bool first) {  // O_t += P_t V
+      auto values = [&](int t, int i, int half, bool first) {  // O_t += P_t V, 64 keys
         const uint32_t va = slot0 + (i % C::SLOTS) * C::TILE;
 #pragma unroll
-        for (int kk = 0; kk < kApTile / 16; ++kk)
+        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
           umma_f16_ta(tmem + 256 + t * D, tmem + t * 128 + kk * 8, umma_desc_mn_sw128(va + kk * 2048, C::BOX),
                       IDESC_O, !(first && kk == 0));
       };
@@ -308,10 +392,13 @@ __global__ void __launch_bounds__(kApThreads, 1)
         const bool more = j + 1 < tl.n;
         ok = kv_wait(vi) && (!more || kv_wait(kn));
         for (int t = 0; t < 2 && ok; ++t) {
-          ok = mbar_wait_live(smem_addr(&sh.p_full[t]), j & 1, &sh.dead);
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = mbar_wait_live(smem_addr(&sh.p_full[t][half]), j & 1, &sh.dead);
+            if (!ok) break;
+            tc_fence_after();
+            values(t, vi, half, j == 0);
+          }
           if (!ok) break;
-          tc_fence_after();
-          values(t, vi, j == 0);
           if (t == 1) umma_commit(smem_addr(&sh.kv_empty[vi % C::SLOTS]));
           // in order behind the product that reads P, whose columns it overwrites
           if (more) scores(t, kn);
@@ -326,8 +413,11 @@ __global__ void __launch_bounds__(kApThreads, 1)
         (void)mbar_wait_bounded(smem_addr(&sh.drain), 0);
       }
     }
+  } else if (wid >= 10) {
+    few_registers();
   } else {
     // -------------------------------------------------- one thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = wid >> 2, row = (wid & 3) * 32 + lane;
     const int tok = t_lo + t * (tokens / 2) + (row >> p.pack_shift);
     const int head = (hg << p.pack_shift) + (row & (p.pack - 1));
@@ -348,18 +438,18 @@ __global__ void __launch_bounds__(kApThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32_wait(r[c]);
       const int key0 = tile_at(tl, j) * kApTile;
-      // columns [0, hi] by position; with a window from lo on, or below sk
+      // visible columns: c <= hi by position; with a window c >= lo or c < sk
       const int hi = pos - key0;
-      const long long lo = p.window > 0 ? (long long)pos - p.window + 1 - key0 : 0;
+      const int lo = p.window > 0 ? hi - p.window + 1 : 0;  // |hi| < 2^31 - window: no overflow
       const int sk = p.n_sink - key0;
-      const bool whole = hi >= kApTile - 1 && (lo <= 0 || sk >= kApTile);
-      if (__any_sync(0xffffffffu, !whole)) {
+      const bool masked = __any_sync(0xffffffffu, !(hi >= kApTile - 1 && (lo <= 0 || sk >= kApTile)));
+      if (masked) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int col = c * 32 + e;
-            if (!(col <= hi && (col >= lo || col < sk))) r[c][e] = 0xff800000u;  // -inf
+            if (col > hi || (col < lo && col >= sk)) r[c][e] = 0xff800000u;  // -inf
           }
       }
       float mx = -INFINITY;
@@ -393,26 +483,27 @@ __global__ void __launch_bounds__(kApThreads, 1)
         }
       }
       const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: 2^-inf = 0
-      float sum0 = 0.f, sum1 = 0.f;
+      const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), neg2 = f2_pack(neg, neg);
+      uint64_t sum = 0;
 #pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t w[32];
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int cc = c + (e >> 4), k = (e & 15) * 2;
-          const float p0 = ex2(__fmaf_rn(__uint_as_float(r[cc][k]), p.scale_log2, neg));
-          const float p1 = ex2(__fmaf_rn(__uint_as_float(r[cc][k + 1]), p.scale_log2, neg));
-          sum0 += p0;
-          sum1 += p1;
-          w[e] = pack_bf16(p0, p1);
+        for (int c = 2 * half; c < 2 * half + 2; ++c) {
+          uint32_t w[16];
+          // (masked columns need a true zero, which only the special function
+          // unit's path gives)
+          if (masked) row_exp2<0>(r[c], scale2, neg2, w, sum);
+          else row_exp2<kApPoly>(r[c], scale2, neg2, w, sum);
+          tmem_st16(s_at + c * 16, w);
         }
-        tmem_st32(s_at + c * 16, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[t][half]));
       }
+      float sum0, sum1;
+      f2_unpack(sum, sum0, sum1);
       l_run += sum0 + sum1;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[t]));
     }
     if (ok) ok = mbar_wait_live(smem_addr(&sh.o_full[t]), 0, &sh.dead);
     ok = __all_sync(0xffffffffu, ok);
