@@ -9,6 +9,7 @@ importing this module without it raises ImportError -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -453,42 +454,67 @@ class TierSim:
 _attn = {}
 
 
+class _Geometry:
+    """Geometry of a context's attention, as the calls compare and pass it."""
+
+    def __init__(self, n_q, n_kv, head_dim, page_size, cache_type, device):
+        self.n_q, self.n_kv, self.dim, self.device = n_q, n_kv, head_dim, device
+        self.batch = (n_kv, head_dim, page_size, cache_type, device)
+
+
+@functools.cache
+def _marshal():
+    """The compiled marshalling of the attention calls, given their addresses."""
+    import torch  # noqa: F401  (its libraries first)
+
+    from . import _marshal as m
+    m.set_calls(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        _lib.moe_qk_norm_rope, _lib.moe_kv_append, _lib.moe_attn_forward, _lib.moe_attn_prefill)))
+    return m
+
+
 def moe_attn_configure(ctx, n_q, n_kv, head_dim, page_size, cache_type):
+    global _m
+    _m = _marshal()
     _check(ctx, _lib.moe_attn_configure(ctx, n_q, n_kv, head_dim, page_size, cache_type))
     import torch
-    _attn[ctx] = (n_q, n_kv, head_dim, page_size, cache_type, torch.cuda.current_device())
+    _attn[ctx] = _Geometry(n_q, n_kv, head_dim, page_size, cache_type, torch.cuda.current_device())
 
 
-def _geometry(ctx):
-    g = _attn.get(ctx)
-    if g is None:
-        raise MoeError(MOE_ERR_STATE, "moe_attn_configure comes first")
-    return g
+def _no_geometry(ctx):
+    raise MoeError(MOE_ERR_STATE, "moe_attn_configure comes first")
+
+
+@functools.cache
+def _dtype(name):
+    import torch
+    return getattr(torch, name)
 
 
 def _dense(name, t, dtype, shape=None):
     """A dense CUDA tensor of this type (and shape); its address."""
-    if not t.is_cuda or str(t.dtype) != "torch." + dtype or not t.is_contiguous():
+    if not t.is_cuda or t.dtype is not _dtype(dtype) or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous CUDA tensor of {dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
     return t.data_ptr()
 
 
-def _head_rows(name, t, n, heads, dim, device):
-    """Rows [n, heads, dim] (or [n, heads * dim]) of 16-bit elements, dense
-    within a row: (address, elements between rows)."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        ok = shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads == 1 or stride[1] == dim)
-    else:
-        ok = len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1
-    if not ok or shape[0] < n or t.element_size() != 2:
-        raise ValueError(f"{name}: bf16 rows [{n}, {heads}, {dim}], dense within a row, not {tuple(shape)}")
-    if not t.is_cuda or t.get_device() != device:
-        raise ValueError(f"{name}: a tensor on the context's device (cuda:{device})")
-    # the stride of a single row means nothing
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * dim)
+def _stream_on(stream, device):
+    """As _stream, with the current stream of `device` for None."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return _raw_stream(device)
+
+
+def _raw_stream(device):
+    """The current stream's handle: torch's own accessor when it has one (a
+    tenth of the time of building a Stream object)."""
+    global _raw_stream
+    import torch
+    fast = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = fast or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
 
 
 class KvBatch:
@@ -510,25 +536,19 @@ class KvBatch:
             raise ValueError("page_table: [n_seqs, max_pages]")
         n_seqs, max_pages = page_table.shape
         tensors = [k, v, page_table, row_off, kv_len, k_scale, v_scale]
-        self.geometry = (n_kv, k.shape[3], k.shape[2], MOE_KV_E4M3 if e4m3 else MOE_KV_BF16)
         self.c = _KvBatch(
             _dense("k", k, kind), _dense("v", v, kind, k.shape),
             None if k_scale is None else _dense("k_scale", k_scale, "float32", (n_kv,)),
             None if v_scale is None else _dense("v_scale", v_scale, "float32", (n_kv,)),
             _dense("page_table", page_table, "int32"), _dense("row_off", row_off, "int32", (n_seqs + 1,)),
             _dense("kv_len", kv_len, "int32", (n_seqs,)), n_pages, n_seqs, max_pages, n_rows)
-        self.device = k.get_device()
-        if any(t is not None and t.get_device() != self.device for t in tensors):
+        device = k.get_device()
+        self.geometry = (n_kv, k.shape[3], k.shape[2], MOE_KV_E4M3 if e4m3 else MOE_KV_BF16, device)
+        if any(t is not None and t.get_device() != device for t in tensors):
             raise ValueError("the batch's tensors are on different devices")
         self.tensors = tensors
         self.n_rows = n_rows
         self.ref = ctypes.addressof(self.c)
-
-    def check(self, g):
-        if self.geometry != (g[1], g[2], g[3], g[4]) or self.device != g[5]:
-            raise ValueError(f"batch of (n_kv, head_dim, page_size, type) {self.geometry} on cuda:{self.device}: "
-                             f"the context has {g[1:5]} on cuda:{g[5]}")
-
 
 class QkNorm:
     """RMSNorm of the query and key heads (moe_qk_norm): fp32 [head_dim] CUDA
@@ -536,14 +556,13 @@ class QkNorm:
 
     def __init__(self, q_gamma=None, k_gamma=None, eps=1e-6):
         self.tensors = [t for t in (q_gamma, k_gamma) if t is not None]
+        kinds = {(t.numel(), t.get_device()) for t in self.tensors}
+        if len(kinds) > 1:
+            raise ValueError("q_gamma and k_gamma: of one length, on one device")
+        self.geometry = kinds.pop() if kinds else None
         self.c = _QkNorm(None if q_gamma is None else _dense("q_gamma", q_gamma, "float32"),
                          None if k_gamma is None else _dense("k_gamma", k_gamma, "float32"), float(eps))
         self.ref = ctypes.addressof(self.c)
-
-    def check(self, g):
-        if any(tuple(t.shape) != (g[2],) or t.get_device() != g[5] for t in self.tensors):
-            raise ValueError(f"norm weights: [{g[2]}] on cuda:{g[5]}")
-
 
 class Rope:
     """Rotary positions (moe_rope): inv_freq float64 [rot_dim / 2] on the GPU,
@@ -551,57 +570,61 @@ class Rope:
 
     def __init__(self, inv_freq, rot_dim, interleaved=False):
         self.tensors = [inv_freq]
+        self.device = inv_freq.get_device()
         self.c = _Rope(_dense("inv_freq", inv_freq, "float64", (rot_dim // 2,)), rot_dim, int(bool(interleaved)))
         self.ref = ctypes.addressof(self.c)
 
-    def check(self, g):
-        if self.tensors[0].get_device() != g[5]:
-            raise ValueError(f"inv_freq: on cuda:{g[5]}")
+def _batch_ref(batch, g):
+    if batch.geometry != g.batch:
+        raise ValueError(f"batch of (n_kv, head_dim, page_size, type, device) {batch.geometry}: the context has "
+                         f"{g.batch}")
+    return batch.ref
 
 
-def _ref(handle, g):
-    if handle is None:
+def _norm_ref(norm, g):
+    if norm is None:
         return None
-    handle.check(g)
-    return handle.ref
+    if norm.geometry is not None and norm.geometry != (g.dim, g.device):
+        raise ValueError(f"norm weights: [{g.dim}] on cuda:{g.device}")
+    return norm.ref
+
+
+def _rope_ref(rope, g):
+    if rope is None:
+        return None
+    if rope.device != g.device:
+        raise ValueError(f"inv_freq: on cuda:{g.device}")
+    return rope.ref
 
 
 def moe_qk_norm_rope(ctx, n_rows, q, k, pos, norm, rope, q_out, k_out, stream=None):
-    g = _geometry(ctx)
-    n_q, n_kv, dim, dev = g[0], g[1], g[2], g[5]
-    if pos is not None:
-        pp = _dense("pos", pos, "int32")
-        if pos.numel() < n_rows or pos.get_device() != dev:
-            raise ValueError(f"pos: int32 [{n_rows}] on cuda:{dev}")
-    else:
-        pp = None
-    _check(ctx, _lib.moe_qk_norm_rope(
-        ctx, n_rows, *_head_rows("q", q, n_rows, n_q, dim, dev), *_head_rows("k", k, n_rows, n_kv, dim, dev), pp,
-        _ref(norm, g), _ref(rope, g), *_head_rows("q_out", q_out, n_rows, n_q, dim, dev),
-        *_head_rows("k_out", k_out, n_rows, n_kv, dim, dev), _stream(stream)))
+    g = _attn.get(ctx) or _no_geometry(ctx)
+    rc = _m.qk_norm_rope(g.n_q, g.n_kv, g.dim, g.device, ctx, n_rows, q, k, pos, _norm_ref(norm, g),
+                         _rope_ref(rope, g), q_out, k_out, _stream_on(stream, g.device))
+    if rc:
+        _check(ctx, rc)
 
 
 def moe_kv_append(ctx, batch, q, k, v, norm, rope, q_out, stream=None):
     """q and q_out may both be None (keys and values only)."""
-    g = _geometry(ctx)
-    n_q, n_kv, dim, dev, n = g[0], g[1], g[2], g[5], batch.n_rows
-    _check(ctx, _lib.moe_kv_append(
-        ctx, _ref(batch, g), *((None, 0) if q is None else _head_rows("q", q, n, n_q, dim, dev)),
-        *_head_rows("k", k, n, n_kv, dim, dev), *_head_rows("v", v, n, n_kv, dim, dev), _ref(norm, g),
-        _ref(rope, g), *((None, 0) if q_out is None else _head_rows("q_out", q_out, n, n_q, dim, dev)),
-        _stream(stream)))
-
-
-def _attend(fn, ctx, batch, q, max_T, scale, window, n_sink, out, stream):
-    g = _geometry(ctx)
-    n_q, dim, dev, n = g[0], g[2], g[5], batch.n_rows
-    _check(ctx, fn(ctx, _ref(batch, g), *_head_rows("q", q, n, n_q, dim, dev), max_T, scale, window, n_sink,
-                   *_head_rows("out", out, n, n_q, dim, dev), _stream(stream)))
+    g = _attn.get(ctx) or _no_geometry(ctx)
+    rc = _m.kv_append(g.n_q, g.n_kv, g.dim, g.device, ctx, batch.n_rows, _batch_ref(batch, g), q, k, v,
+                      _norm_ref(norm, g), _rope_ref(rope, g), q_out, _stream_on(stream, g.device))
+    if rc:
+        _check(ctx, rc)
 
 
 def moe_attn_forward(ctx, batch, q, max_T, scale, window, n_sink, out, stream=None):
-    _attend(_lib.moe_attn_forward, ctx, batch, q, max_T, scale, window, n_sink, out, stream)
+    g = _attn.get(ctx) or _no_geometry(ctx)
+    rc = _m.attend(0, g.n_q, g.dim, g.device, ctx, batch.n_rows, _batch_ref(batch, g), q, max_T, scale, window,
+                   n_sink, out, _stream_on(stream, g.device))
+    if rc:
+        _check(ctx, rc)
 
 
 def moe_attn_prefill(ctx, batch, q, max_T, scale, window, n_sink, out, stream=None):
-    _attend(_lib.moe_attn_prefill, ctx, batch, q, max_T, scale, window, n_sink, out, stream)
+    g = _attn.get(ctx) or _no_geometry(ctx)
+    rc = _m.attend(1, g.n_q, g.dim, g.device, ctx, batch.n_rows, _batch_ref(batch, g), q, max_T, scale, window,
+                   n_sink, out, _stream_on(stream, g.device))
+    if rc:
+        _check(ctx, rc)

@@ -145,6 +145,32 @@ MOE_DEV float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Bounded wait of one thread that also ends when the block gave up (`dead`).
+// Each try may suspend the thread for up to 50 us (a poll without that hint
+// returns at once and asks again, and a few such pollers hold up every other
+// barrier operation of the SM), so the limit is about a second.
+MOE_DEV bool mbar_wait_live(uint32_t bar, uint32_t parity, const int *dead) {
+  for (uint32_t i = 0; i < 20000; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(50000)
+        : "memory");
+    if (ok) return true;
+    if (dead && *reinterpret_cast<const volatile int *>(dead)) return false;
+  }
+  return false;
+}
+// The same for a whole warp: one lane polls.  (32 lanes polling one barrier
+// are served one after another and hold up every other barrier of the SM.)
+MOE_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, const int *dead) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait_live(bar, parity, dead);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
 MOE_DEV void bar_sync_n(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 MOE_DEV void tma_box_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t policy) {
   asm volatile(
@@ -295,9 +321,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       const int st = (int)(issued % S);
       const uint32_t use = (uint32_t)(issued / S);
       const uint32_t bar = smem_addr(&sh.full[st]);
-      bool ok = true;
-      if (use > 0) ok = mbar_wait_bounded(smem_addr(&sh.empty[st]), (use - 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) {
+      if (use > 0 && !mbar_wait_warp(smem_addr(&sh.empty[st]), (use - 1) & 1, &sh.dead)) {
         if (lane == 0) give_up();
         break;
       }
@@ -332,6 +356,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   const int g = lane >> 2, cq = lane & 3;
   long long n_done = 0;
   long long u = u0;
+  bool live = true;  // false once a wait of this warp gave up: it goes on through the shared barriers
   while (u < u1) {
     // this block's share of one (sequence, head, row block)
     const int kv_h = c.seg / c.nblk, blk = c.seg % c.nblk;
@@ -416,9 +441,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     for (int k = k_beg; k < k_end; ++k, ++n_done) {
       const int st = (int)(n_done % S);
       const uint32_t use = (uint32_t)(n_done / S);
-      bool ok = !dead();
-      if (ok) ok = mbar_wait_bounded(smem_addr(&sh.full[st]), use & 1);
-      if (__all_sync(0xffffffffu, ok)) {
+      live = live && mbar_wait_warp(smem_addr(&sh.full[st]), use & 1, &sh.dead);
+      if (live) {
         const int tile = tile_at(c.t, k);
         const int key0 = tile * kAtTile + kg * KEYS;  // first key of this warp
         const uint32_t kt = stage0 + (uint32_t)(st * 2) * C::TILE, vt = kt + C::TILE;

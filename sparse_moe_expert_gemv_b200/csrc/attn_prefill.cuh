@@ -33,7 +33,7 @@ namespace moe {
 constexpr int kApTile = 128;   // keys of a tile
 constexpr int kApRows = 256;   // rows of a block
 constexpr int kApThreads = 384;  // warps 10 and 11 only give up registers
-constexpr int kApPoly = 1;      // of four pairs of exponentials, those on the FMA units
+constexpr int kApPoly = 0;      // of four pairs of exponentials, those on the FMA units
 constexpr float kApSlack = 8.f;  // log2 of the growth that O is not rescaled for
 
 template <int D>
@@ -64,15 +64,6 @@ struct AttnPfShared {
   int dead;
 };
 static_assert(sizeof(AttnPfShared) <= 1024, "fits the block before the tiles");
-
-// Bounded wait that also ends when another warp of the block gave up.
-MOE_DEV bool mbar_wait_live(uint32_t bar, uint32_t parity, const int *dead) {
-  for (uint32_t i = 0; i < (1u << 20); ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*reinterpret_cast<const volatile int *>(dead)) return false;
-  }
-  return false;
-}
 
 // Descriptor of an MN-major tile with 128-byte swizzle: lines of 64 columns,
 // one line per key; 8-key groups are 1024 B apart (stride offset), 64-column
@@ -296,42 +287,48 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const long long lo = p.window > 0 ? (long long)pos0 - p.window + 1 : 0;
     const int sink_end = lo > 0 ? (int)min((long long)p.n_sink, lo) : 0;
     const int my_page = lane / C::HALVES, my_half = lane % C::HALVES;
-    // the page of this lane's box in tile j, or -1 when no row sees a key of it
-    auto page_of = [&](int j) {
-      const int first_key = tile_at(tl, j) * kApTile + my_page * pr;
-      if (lane >= ppt * C::HALVES || !keys_seen(s, p.window, p.n_sink, first_key, pr)) return -1;
-      int page = __ldg(p.page_table + (long long)b * p.max_pages + (first_key >> p.page_shift));
-      if ((unsigned)page >= (unsigned)p.n_pages) {
+    // 32 entries of the page table, one per lane, and the 32 behind them
+    // already on their way: a look-up is never waited for between tiles
+    const int n_pg = (s.kv + p.page - 1) >> p.page_shift;  // pages that hold keys
+    const int *table = p.page_table + (long long)b * p.max_pages;
+    auto entries = [&](int at) { return at + lane < n_pg ? __ldg(table + at + lane) : 0; };
+    int held_at = 0, held = 0, ahead = 0;
+    bool held_any = false;
+    int issued = 0, edge_uses = 0;
+    bool ok = true;
+    for (int j = 0; j < tl.n && ok; ++j) {
+      const int key0 = tile_at(tl, j) * kApTile, pg0 = key0 >> p.page_shift;
+      if (!held_any || pg0 + ppt > held_at + 32) {
+        const bool on = held_any && pg0 == held_at + 32;
+        held = on ? ahead : entries(pg0);
+        held_at = pg0;
+        held_any = true;
+        ahead = entries(pg0 + 32);
+      }
+      const int first_key = key0 + my_page * pr;
+      int page = __shfl_sync(0xffffffffu, held, min(pg0 - held_at + my_page, 31));
+      const bool need = lane < ppt * C::HALVES && keys_seen(s, p.window, p.n_sink, first_key, pr);
+      if (need && (unsigned)page >= (unsigned)p.n_pages) {
         atomicOr(p.status, kErrBadPage);
         page = 0;  // an in-bounds page; the call's result is reported as bad
       }
-      return page;
-    };
-    int issued = 0, edge_uses = 0;
-    bool ok = true;
-    int next = page_of(0);
-    for (int j = 0; j < tl.n && ok; ++j) {
-      const int page = next;
-      if (j + 1 < tl.n) next = page_of(j + 1);  // on its way while this tile's slots come free
-      const int key0 = tile_at(tl, j) * kApTile;
-      const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
-      const int y = (page * p.n_kv + kv_h) * p.page + ((key0 + my_page * pr) & (p.page - 1));
+      const int boxes = __popc(__ballot_sync(0xffffffffu, need));
+      const int y = (page * p.n_kv + kv_h) * p.page + (first_key & (p.page - 1));
       for (int is_v = 0; is_v < 2 && ok; ++is_v, ++issued) {
         const int st = issued % C::SLOTS, use = issued / C::SLOTS;
         // values no row of the sequence sees may hold anything: such rows of
         // the tile become zeros before the tensor cores read them
         const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < lo && key0 + kApTile > sink_end));
-        if (use > 0) ok = mbar_wait_live(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
-        ok = __all_sync(0xffffffffu, ok);
+        if (use > 0) ok = mbar_wait_warp(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
         if (!ok) break;
         const uint32_t full = smem_addr(&sh.kv_full[st]), bar = edge ? smem_addr(&sh.edge) : full;
         const uint32_t dst = slot0 + st * C::TILE;
         if (lane == 0) mbar_expect_tx(bar, (uint32_t)boxes * pr * 128);
         __syncwarp();
-        if (page >= 0)
+        if (need)
           tma_load_2d(dst + my_half * C::BOX + my_page * pr * 128, is_v ? &vmap : &kmap, my_half * 64, y, bar);
         if (edge) {
-          ok = mbar_wait_bounded(bar, edge_uses & 1);
+          ok = mbar_wait_warp(bar, edge_uses & 1, nullptr);
           ++edge_uses;
           for (int r = 0; r < kApTile; ++r) {
             const int k = key0 + r;
@@ -344,7 +341,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
                            : "memory");
           }
           fence_proxy_async_smem();
-          ok = __all_sync(0xffffffffu, ok);
+          __syncwarp();
           if (lane == 0) mbar_arrive(full);
         }
       }
@@ -428,8 +425,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
     float m_ref = -INFINITY, l_run = 0.f;  // m_ref in units of the scores times scale_log2
     bool ok = true;
     for (int j = 0; j < tl.n; ++j) {
-      ok = mbar_wait_live(smem_addr(&sh.s_full[t]), j & 1, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = mbar_wait_warp(smem_addr(&sh.s_full[t]), j & 1, &sh.dead);
       if (!ok) break;
       tc_fence_after();
       uint32_t r[4][32];
@@ -505,8 +501,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
       f2_unpack(sum, sum0, sum1);
       l_run += sum0 + sum1;
     }
-    if (ok) ok = mbar_wait_live(smem_addr(&sh.o_full[t]), 0, &sh.dead);
-    ok = __all_sync(0xffffffffu, ok);
+    if (ok) ok = mbar_wait_warp(smem_addr(&sh.o_full[t]), 0, &sh.dead);
     if (ok) {
       tc_fence_after();
       const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;

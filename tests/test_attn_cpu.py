@@ -49,10 +49,20 @@ def test_binding_refuses_what_the_library_cannot_see(B):
         B.Rope(torch.ones(32, dtype=torch.float64), 64)
     with pytest.raises(ValueError):
         B.QkNorm(torch.ones(64))
-    for bad in (torch.zeros((2, 8, 64), dtype=bf), torch.zeros((2, 8, 64)), torch.zeros((2, 7, 64), dtype=bf),
+    m, batch = B._marshal(), 64  # no call gets as far as its batch
+    good = torch.zeros((2, 8, 64), dtype=bf)  # but for where it lives
+    for bad in (good, torch.zeros((2, 8, 64)), torch.zeros((2, 7, 64), dtype=bf), good.flatten(), 7, None,
                 torch.zeros((2, 8, 128), dtype=bf)[..., ::2]):
         with pytest.raises(ValueError):
-            B._head_rows("q", bad, 2, 8, 64, 0)
+            m.attend(0, 8, 64, 0, 0, 2, batch, bad, 2, 0.1, 0, 0, good, 0)
+        with pytest.raises(ValueError):
+            m.kv_append(8, 8, 64, 0, 0, 2, batch, None, bad, good, None, None, None, 0)
+        with pytest.raises(ValueError):
+            m.qk_norm_rope(8, 8, 64, 0, 0, 2, bad, good, None, None, None, good, good, 0)
+    with pytest.raises(OverflowError):
+        m.attend(0, 8, 64, 0, 0, 2, batch, good, 2, 0.1, 1 << 31, 0, good, 0)
+    with pytest.raises(TypeError):
+        m.attend(0, 8, 64)
     with pytest.raises(B.MoeError) as ei:
         B.moe_qk_norm_rope(12345, 1, None, None, None, None, None, None, None)
     assert ei.value.status == B.MOE_ERR_STATE
