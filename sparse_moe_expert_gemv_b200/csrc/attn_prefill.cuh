@@ -8,21 +8,26 @@
 // A block takes 256 rows: two 128-row tiles, each the rows of `pack` query
 // heads of one KV head (the largest power of two dividing the group) at 128 /
 // pack consecutive tokens, so few tokens of a tile lie above the diagonal.
-// Ten warps:
-//   8     TMA: the query tiles, then key and value tiles of 128 keys through
-//         a ring of slots (one box per page and 64 columns);
-//   9     issues the MMAs: S = Q K^T into tensor memory, O += P V with P read
-//         from tensor memory and V as it lies in the cache ([key][column]: an
-//         MN-major operand);
-//   0-3, 4-7  one thread per row of tile 0 and 1: reads its row of S, masks,
-//         keeps the running maximum and sum, and writes P (bf16) over S.
-// The two tiles alternate: while the tensor cores work for one, the other's
-// rows go through the exponentials.  O stays in tensor memory; it is rescaled
-// only when a row's maximum grew by more than 2^8 over the reference its
-// terms were scaled by (P then holds values up to 2^8, exact to bf16's step
-// like any other; sums are fp32).
+// Warps:
+//   8      TMA: the query tiles and the first keys, then pairs of a value tile
+//          and the next key tile (128 keys each) through a ring (one box per
+//          page and 64 columns);
+//   9, 10  issue the MMAs of tile 0 and 1: S = Q K^T into tensor memory, O +=
+//          P V with P read from tensor memory and V as it lies in the cache
+//          ([key][column]: an MN-major operand).  Issuing is paced by the
+//          tensor cores, so each tile has an issuer of its own: one's waits
+//          are covered by the other's products;
+//   0-3, 4-7  one thread per row of tile 0 and 1, 64 keys a step: reads its
+//          row of S, masks, keeps the running maximum and sum, and writes P
+//          (bf16) over S.
+// S of a tile has two buffers of 64 keys, so the scores of the next step are
+// there while the rows of the present one go through the exponentials.  O
+// stays in tensor memory; it is rescaled only when a row's maximum grew by
+// more than 2^8 over the reference its terms were scaled by (P then holds
+// values up to 2^8, rounded to bf16 like any other; sums are fp32).
 //
-// Tensor memory: S0, S1 (128 columns each, P over the first 64), O0, O1.
+// Tensor memory: S0, S1 (2 x 64 columns each, P over the first 32 of a
+// buffer), O0, O1.
 #pragma once
 
 #include "attn.cuh"
@@ -32,8 +37,8 @@ namespace moe {
 
 constexpr int kApTile = 128;   // keys of a tile
 constexpr int kApRows = 256;   // rows of a block
-constexpr int kApThreads = 384;  // warps 10 and 11 only give up registers
-constexpr int kApPoly = 0;      // of four pairs of exponentials, those on the FMA units
+constexpr int kApThreads = 384;  // warp 11 only gives up registers
+constexpr int kApPoly = 1;      // of four pairs of exponentials, those on the FMA units
 constexpr float kApSlack = 8.f;  // log2 of the growth that O is not rescaled for
 
 template <int D>
@@ -41,8 +46,8 @@ struct AttnPfCfg {
   static constexpr int HALVES = D / 64;                // 128-byte column boxes
   static constexpr int BOX = kApTile * 128;            // 128 rows x 64 columns
   static constexpr int TILE = HALVES * BOX;            // a query, key or value tile
-  static constexpr int SLOTS = D == 128 ? 5 : 8;
-  static constexpr int SMEM = 1024 + 2 * TILE + SLOTS * TILE;
+  static constexpr int PAIRS = D == 128 ? 2 : 4;       // ring of (value tile, next key tile)
+  static constexpr int SMEM = 1024 + 2 * TILE + (1 + 2 * PAIRS) * TILE;
 };
 
 struct AttnPfParams {
@@ -57,7 +62,7 @@ struct AttnPfParams {
 };
 
 struct AttnPfShared {
-  unsigned long long q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2][2], o_full[2], edge, drain;
+  unsigned long long q_full, kv_full[4], kv_empty[4], s_full[2][2], p_full[2][2], o_done[2], o_full[2], edge, drain[2];
   long long scan[kApThreads / 32];
   uint32_t tmem;
   int item[2];  // sequence, row block
@@ -173,6 +178,11 @@ MOE_DEV void row_exp2(const uint32_t (&r)[32], uint64_t scale, uint64_t neg, uin
   }
 }
 
+// Bytes still to come on a barrier, without an arrival.
+MOE_DEV void mbar_expect_only(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kApThreads, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
   extern __shared__ __align__(1024) unsigned char ap_smem[];
   AttnPfShared &sh = *reinterpret_cast<AttnPfShared *>(ap_smem);
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
-  const uint32_t q0 = smem_addr(ap_smem) + 1024, slot0 = q0 + 2 * C::TILE;
+  const uint32_t q0 = smem_addr(ap_smem) + 1024, kfirst = q0 + 2 * C::TILE, slot0 = kfirst + C::TILE;
   pdl_wait();
 
   // ---- this block's item: head group fastest (blocks that share keys run
@@ -228,18 +238,20 @@ __global__ void __launch_bounds__(kApThreads, 1)
   }
   if (tid == 0) {
     mbar_init(smem_addr(&sh.q_full), 1);
-    for (int i = 0; i < C::SLOTS; ++i) {
+    for (int i = 0; i < C::PAIRS; ++i) {
       mbar_init(smem_addr(&sh.kv_full[i]), 1);
-      mbar_init(smem_addr(&sh.kv_empty[i]), 1);
+      mbar_init(smem_addr(&sh.kv_empty[i]), 2);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_addr(&sh.s_full[t]), 1);
-      mbar_init(smem_addr(&sh.p_full[t][0]), 4);
-      mbar_init(smem_addr(&sh.p_full[t][1]), 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_addr(&sh.s_full[t][h]), 1);
+        mbar_init(smem_addr(&sh.p_full[t][h]), 4);
+      }
+      mbar_init(smem_addr(&sh.o_done[t]), 1);
       mbar_init(smem_addr(&sh.o_full[t]), 1);
+      mbar_init(smem_addr(&sh.drain[t]), 1);
     }
     mbar_init(smem_addr(&sh.edge), 1);
-    mbar_init(smem_addr(&sh.drain), 1);
     sh.dead = 0;
     fence_mbar_init();
   }
@@ -275,14 +287,6 @@ __global__ void __launch_bounds__(kApThreads, 1)
     few_registers();
     const int pr = min(p.page, kApTile);
     const int ppt = kApTile / pr;  // boxes along a tile's keys, at most 8
-    if (lane == 0) {
-      const uint32_t bar = smem_addr(&sh.q_full);
-      mbar_expect_tx(bar, 2 * C::TILE);
-      for (int t = 0; t < 2; ++t)
-        for (int h = 0; h < C::HALVES; ++h)
-          tma_load_3d(q0 + t * C::TILE + h * C::BOX, &qmap, h * 64, hg << p.pack_shift,
-                      s.row0 + t_lo + t * (tokens / 2), bar);
-    }
     // keys that some row of the sequence sees: [0, sink_end) and [lo, kv)
     const long long lo = p.window > 0 ? (long long)pos0 - p.window + 1 : 0;
     const int sink_end = lo > 0 ? (int)min((long long)p.n_sink, lo) : 0;
@@ -292,125 +296,144 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const int n_pg = (s.kv + p.page - 1) >> p.page_shift;  // pages that hold keys
     const int *table = p.page_table + (long long)b * p.max_pages;
     auto entries = [&](int at) { return at + lane < n_pg ? __ldg(table + at + lane) : 0; };
-    int held_at = 0, held = 0, ahead = 0;
-    bool held_any = false;
-    int issued = 0, edge_uses = 0;
-    bool ok = true;
-    for (int j = 0; j < tl.n && ok; ++j) {
+    int held_at = -64, held = 0, ahead = 0;
+    // this lane's box of tile j: whether its page holds a key that is seen,
+    // and its row in the cache
+    auto box_of = [&](int j, bool &need, int &y) {
       const int key0 = tile_at(tl, j) * kApTile, pg0 = key0 >> p.page_shift;
-      if (!held_any || pg0 + ppt > held_at + 32) {
-        const bool on = held_any && pg0 == held_at + 32;
-        held = on ? ahead : entries(pg0);
+      if (pg0 + ppt > held_at + 32) {
+        held = pg0 == held_at + 32 ? ahead : entries(pg0);
         held_at = pg0;
-        held_any = true;
         ahead = entries(pg0 + 32);
       }
       const int first_key = key0 + my_page * pr;
       int page = __shfl_sync(0xffffffffu, held, min(pg0 - held_at + my_page, 31));
-      const bool need = lane < ppt * C::HALVES && keys_seen(s, p.window, p.n_sink, first_key, pr);
+      need = lane < ppt * C::HALVES && keys_seen(s, p.window, p.n_sink, first_key, pr);
       if (need && (unsigned)page >= (unsigned)p.n_pages) {
         atomicOr(p.status, kErrBadPage);
         page = 0;  // an in-bounds page; the call's result is reported as bad
       }
-      const int boxes = __popc(__ballot_sync(0xffffffffu, need));
-      const int y = (page * p.n_kv + kv_h) * p.page + (first_key & (p.page - 1));
-      for (int is_v = 0; is_v < 2 && ok; ++is_v, ++issued) {
-        const int st = issued % C::SLOTS, use = issued / C::SLOTS;
-        // values no row of the sequence sees may hold anything: such rows of
-        // the tile become zeros before the tensor cores read them
-        const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < lo && key0 + kApTile > sink_end));
-        if (use > 0) ok = mbar_wait_warp(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
-        if (!ok) break;
-        const uint32_t full = smem_addr(&sh.kv_full[st]), bar = edge ? smem_addr(&sh.edge) : full;
-        const uint32_t dst = slot0 + st * C::TILE;
-        if (lane == 0) mbar_expect_tx(bar, (uint32_t)boxes * pr * 128);
-        __syncwarp();
-        if (need)
-          tma_load_2d(dst + my_half * C::BOX + my_page * pr * 128, is_v ? &vmap : &kmap, my_half * 64, y, bar);
+      y = (page * p.n_kv + kv_h) * p.page + (first_key & (p.page - 1));
+    };
+    const uint32_t box_at = my_half * C::BOX + my_page * pr * 128;
+    auto bytes_of = [&](bool need) { return (uint32_t)__popc(__ballot_sync(0xffffffffu, need)) * pr * 128; };
+    bool need, need_k;
+    int y, y_k;
+    box_of(0, need, y);
+    const uint32_t bytes0 = bytes_of(need), q_bar = smem_addr(&sh.q_full);
+    if (lane == 0) {  // the queries and the first keys
+      mbar_expect_tx(q_bar, 2 * C::TILE + bytes0);
+      for (int t = 0; t < 2; ++t)
+        for (int h = 0; h < C::HALVES; ++h)
+          tma_load_3d(q0 + t * C::TILE + h * C::BOX, &qmap, h * 64, hg << p.pack_shift,
+                      s.row0 + t_lo + t * (tokens / 2), q_bar);
+    }
+    __syncwarp();
+    if (need) tma_load_2d(kfirst + box_at, &kmap, my_half * 64, y, q_bar);
+    int issued = 0, edge_uses = 0;
+    bool ok = true;
+    for (int j = 0; j < tl.n; ++j) {
+      const int key0 = tile_at(tl, j) * kApTile;
+      need_k = false;
+      if (j + 1 < tl.n) box_of(j + 1, need_k, y_k);
+      const int st = j % C::PAIRS, use = j / C::PAIRS;
+      // values no row of the sequence sees may hold anything: such rows of
+      // the tile become zeros before the tensor cores read them
+      const bool edge = key0 + kApTile > s.kv || (key0 < lo && key0 + kApTile > sink_end);
+      const uint32_t bytes_v = bytes_of(need), bytes_k = bytes_of(need_k);
+      if (use > 0) ok = mbar_wait_warp(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
+      if (!ok) break;
+      const uint32_t full = smem_addr(&sh.kv_full[st]), bar = edge ? smem_addr(&sh.edge) : full;
+      const uint32_t dst = slot0 + st * 2 * C::TILE;
+      if (lane == 0) {
         if (edge) {
-          ok = mbar_wait_warp(bar, edge_uses & 1, nullptr);
-          ++edge_uses;
-          for (int r = 0; r < kApTile; ++r) {
-            const int k = key0 + r;
-            if (k < s.kv && (k < sink_end || k >= lo)) continue;
-            // a key's line in each half: 8 16-byte pieces
-            if (lane < 8 * C::HALVES)
-              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (lane >> 3) * C::BOX + r * 128 +
-                                                                         (lane & 7) * 16),
-                           "r"(0)
-                           : "memory");
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full);
+          mbar_expect_tx(bar, bytes_v);
+          mbar_expect_only(full, bytes_k);  // the arrival follows when the values are in order
+        } else {
+          mbar_expect_tx(full, bytes_v + bytes_k);
         }
       }
+      __syncwarp();
+      if (need) tma_load_2d(dst + box_at, &vmap, my_half * 64, y, bar);
+      if (need_k) tma_load_2d(dst + C::TILE + box_at, &kmap, my_half * 64, y_k, full);
+      ++issued;
+      if (edge) {
+        ok = mbar_wait_warp(bar, edge_uses & 1, nullptr);
+        ++edge_uses;
+        for (int r = 0; r < kApTile; ++r) {
+          const int k = key0 + r;
+          if (k < s.kv && (k < sink_end || k >= lo)) continue;
+          // a key's line in each half: 8 16-byte pieces
+          if (lane < 8 * C::HALVES)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (lane >> 3) * C::BOX + r * 128 +
+                                                                       (lane & 7) * 16),
+                         "r"(0)
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+      }
+      need = need_k;
+      y = y_k;
     }
     if (!ok && lane == 0) give_up();
     // no tile may land after the block has gone
-    (void)mbar_wait_bounded(smem_addr(&sh.q_full), 0);
-    for (int i = max(0, issued - C::SLOTS); i < issued; ++i)
-      (void)mbar_wait_bounded(smem_addr(&sh.kv_full[i % C::SLOTS]), (i / C::SLOTS) & 1);
-  } else if (wid == 9) {
-    // -------------------------------------------------------- MMA issuer
+    (void)mbar_wait_bounded(q_bar, 0);
+    for (int j = max(0, issued - C::PAIRS); j < issued; ++j)
+      (void)mbar_wait_bounded(smem_addr(&sh.kv_full[j % C::PAIRS]), (j / C::PAIRS) & 1);
+  } else if (wid == 9 || wid == 10) {
+    // ------------------------------------- MMA issuers, one per row tile
     few_registers();
     if (lane == 0) {
-      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kApTile);
+      const int t = wid - 9;
+      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, 64);
       constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
-      bool ok = mbar_wait_live(smem_addr(&sh.q_full), 0, &sh.dead);
-      auto kv_wait = [&](int i) {
-        return mbar_wait_live(smem_addr(&sh.kv_full[i % C::SLOTS]), (i / C::SLOTS) & 1, &sh.dead);
-      };
-      auto scores = [&](int t, int i) {  // S_t = Q_t K^T, the key tile in slot i
-        const uint32_t qa = q0 + t * C::TILE, ka = slot0 + (i % C::SLOTS) * C::TILE;
+      const uint32_t s_at = tmem + t * 128, o_at = tmem + 256 + t * D;
+      const uint64_t qd = umma_desc_sw128(q0 + t * C::TILE);
+      auto scores = [&](uint32_t ka, int h) {  // S_h = Q K^T, 64 keys
+        const uint64_t kd = umma_desc_sw128(ka + h * 64 * 128);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::BOX + (kk & 3) * 32;
-          umma_f16(tmem + t * 128, umma_desc_sw128(qa + off), umma_desc_sw128(ka + off), IDESC_S, kk != 0);
+          constexpr int box = C::BOX >> 4;
+          umma_f16(s_at + h * 64, qd + (kk >> 2) * box + (kk & 3) * 2, kd + (kk >> 2) * box + (kk & 3) * 2, IDESC_S,
+                   kk != 0);
         }
-        umma_commit(smem_addr(&sh.s_full[t]));
+        umma_commit(smem_addr(&sh.s_full[t][h]));
       };
-      auto values = [&](int t, int i, int half, bool first) {  // O_t += P_t V, 64 keys
-        const uint32_t va = slot0 + (i % C::SLOTS) * C::TILE;
-#pragma unroll
-        for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-          umma_f16_ta(tmem + 256 + t * D, tmem + t * 128 + kk * 8, umma_desc_mn_sw128(va + kk * 2048, C::BOX),
-                      IDESC_O, !(first && kk == 0));
-      };
-      ok = ok && kv_wait(0);
+      bool ok = mbar_wait_live(smem_addr(&sh.q_full), 0, &sh.dead);
       if (ok) {
         tc_fence_after();
-        scores(0, 0);
-        scores(1, 0);
-        umma_commit(smem_addr(&sh.kv_empty[0]));
+        scores(kfirst, 0);
+        scores(kfirst, 1);
       }
       for (int j = 0; j < tl.n && ok; ++j) {
-        const int vi = 2 * j + 1, kn = 2 * j + 2;
-        const bool more = j + 1 < tl.n;
-        ok = kv_wait(vi) && (!more || kv_wait(kn));
-        for (int t = 0; t < 2 && ok; ++t) {
-          for (int half = 0; half < 2 && ok; ++half) {
-            ok = mbar_wait_live(smem_addr(&sh.p_full[t][half]), j & 1, &sh.dead);
-            if (!ok) break;
-            tc_fence_after();
-            values(t, vi, half, j == 0);
-          }
+        const int st = j % C::PAIRS;
+        const uint32_t va = slot0 + st * 2 * C::TILE;
+        const uint64_t vd = umma_desc_mn_sw128(va, C::BOX);
+        ok = mbar_wait_live(smem_addr(&sh.kv_full[st]), (j / C::PAIRS) & 1, &sh.dead);
+        for (int h = 0; h < 2 && ok; ++h) {
+          ok = mbar_wait_live(smem_addr(&sh.p_full[t][h]), j & 1, &sh.dead);
           if (!ok) break;
-          if (t == 1) umma_commit(smem_addr(&sh.kv_empty[vi % C::SLOTS]));
-          // in order behind the product that reads P, whose columns it overwrites
-          if (more) scores(t, kn);
-          else umma_commit(smem_addr(&sh.o_full[t]));
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // O += P_h V, 64 keys
+            umma_f16_ta(o_at, s_at + h * 64 + kk * 8, vd + (h * 4 + kk) * (2048 >> 4), IDESC_O, (j | h | kk) != 0);
+          umma_commit(smem_addr(&sh.o_done[t]));
+          // in order behind the product that reads P_h, whose columns it overwrites
+          if (j + 1 < tl.n) scores(va + C::TILE, h);
         }
-        if (more && ok) umma_commit(smem_addr(&sh.kv_empty[kn % C::SLOTS]));
+        if (ok) umma_commit(smem_addr(&sh.kv_empty[st]));
       }
+      umma_commit(smem_addr(&sh.o_full[t]));
       if (!ok) {
         give_up();
         // every issued MMA is complete before tensor memory is released
-        umma_commit(smem_addr(&sh.drain));
-        (void)mbar_wait_bounded(smem_addr(&sh.drain), 0);
+        umma_commit(smem_addr(&sh.drain[t]));
+        (void)mbar_wait_bounded(smem_addr(&sh.drain[t]), 0);
       }
     }
-  } else if (wid >= 10) {
+  } else if (wid == 11) {
     few_registers();
   } else {
     // -------------------------------------------------- one thread per row
@@ -424,49 +447,49 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * D;
     float m_ref = -INFINITY, l_run = 0.f;  // m_ref in units of the scores times scale_log2
     bool ok = true;
-    for (int j = 0; j < tl.n; ++j) {
-      ok = mbar_wait_warp(smem_addr(&sh.s_full[t]), j & 1, &sh.dead);
+    for (int i = 0; i < 2 * tl.n; ++i) {  // 64 keys a step
+      const int h = i & 1, j = i >> 1;
+      ok = mbar_wait_warp(smem_addr(&sh.s_full[t][h]), j & 1, &sh.dead);
       if (!ok) break;
       tc_fence_after();
-      uint32_t r[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_issue(s_at + c * 32, r[c]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_wait(r[c]);
-      const int key0 = tile_at(tl, j) * kApTile;
+      uint32_t r[2][32];
+      tmem_ld32_issue(s_at + h * 64, r[0]);
+      tmem_ld32_issue(s_at + h * 64 + 32, r[1]);
+      const int key0 = tile_at(tl, j) * kApTile + h * 64;
       // visible columns: c <= hi by position; with a window c >= lo or c < sk
       const int hi = pos - key0;
       const int lo = p.window > 0 ? hi - p.window + 1 : 0;  // |hi| < 2^31 - window: no overflow
       const int sk = p.n_sink - key0;
-      const bool masked = __any_sync(0xffffffffu, !(hi >= kApTile - 1 && (lo <= 0 || sk >= kApTile)));
+      const bool masked = __any_sync(0xffffffffu, !(hi >= 63 && (lo <= 0 || sk >= 64)));
+      tmem_ld32_wait(r[0]);
+      tmem_ld32_wait(r[1]);
       if (masked) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = c * 32 + e;
-            if (col > hi || (col < lo && col >= sk)) r[c][e] = 0xff800000u;  // -inf
-          }
+        for (int c = 0; c < 64; ++c)
+          if (c > hi || (c < lo && c >= sk)) r[c >> 5][c & 31] = 0xff800000u;  // -inf
       }
-      float mx = -INFINITY;
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 64; c += 8)
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          mx = fmaxf(mx, fmaxf(__uint_as_float(r[c][e]), __uint_as_float(r[c][e + 1])));
-      mx *= p.scale_log2;
-      // the reference follows the maximum when it fell 2^kApSlack behind (the
-      // commit that brought S also says that O holds every earlier product)
-      const bool first = m_ref == -INFINITY;
-      const bool grow = mx > m_ref + kApSlack;
+        for (int e = 0; e < 4; ++e)
+          m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(r[c >> 5][(c & 31) + 2 * e]),
+                                     __uint_as_float(r[c >> 5][(c & 31) + 2 * e + 1])));
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+      // the reference follows the maximum when it fell 2^kApSlack behind
       float corr = 1.f;
-      if (first) {
+      if (m_ref == -INFINITY) {
         m_ref = mx;
-      } else if (grow) {
+      } else if (mx > m_ref + kApSlack) {
         corr = ex2(m_ref - mx);
         m_ref = mx;
       }
-      if (__any_sync(0xffffffffu, corr != 1.f)) {
+      if (__any_sync(0xffffffffu, corr != 1.f)) {  // (never in the first step)
+        // O holds every earlier product once the last one is through, and the
+        // next one waits for the P of this step
+        ok = mbar_wait_warp(smem_addr(&sh.o_done[t]), (i - 1) & 1, &sh.dead);
+        if (!ok) break;
+        tc_fence_after();
         l_run *= corr;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -482,21 +505,18 @@ __global__ void __launch_bounds__(kApThreads, 1)
       const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), neg2 = f2_pack(neg, neg);
       uint64_t sum = 0;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int c = 2 * half; c < 2 * half + 2; ++c) {
-          uint32_t w[16];
-          // (masked columns need a true zero, which only the special function
-          // unit's path gives)
-          if (masked) row_exp2<0>(r[c], scale2, neg2, w, sum);
-          else row_exp2<kApPoly>(r[c], scale2, neg2, w, sum);
-          tmem_st16(s_at + c * 16, w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[t][half]));
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+        // (masked columns need a true zero, which only the special function
+        // unit's path gives)
+        if (masked) row_exp2<0>(r[c], scale2, neg2, w, sum);
+        else row_exp2<kApPoly>(r[c], scale2, neg2, w, sum);
+        tmem_st16(s_at + h * 64 + c * 16, w);
       }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[t][h]));
       float sum0, sum1;
       f2_unpack(sum, sum0, sum1);
       l_run += sum0 + sum1;
