@@ -105,25 +105,23 @@ MOE_HOST_DEV_INLINE long long run_length(long long total, long long grid, long l
 MOE_DEV void ldsm_x4(uint32_t a, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 MOE_DEV void ldsm_x4_t(uint32_t a, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 template <bool F16>
 MOE_DEV void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (F16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -448,30 +446,33 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         const uint32_t kt = stage0 + (uint32_t)(st * 2) * C::TILE, vt = kt + C::TILE;
         // ---- scores
         float sc[NT][4];
+        uint32_t kb[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        // (the keys' tiles inside, so that NT products are in flight)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          // four 8-key x 16-byte matrices of consecutive 16-byte columns
-          const int key = kg * KEYS + n * 8 + (lane & 7);
+        for (int ch = 0; ch < C::ROWB / 16; ch += 4) {
 #pragma unroll
-          for (int ch = 0; ch < C::ROWB / 16; ch += 4) {
+          for (int n = 0; n < NT; ++n) {
+            // four 8-key x 16-byte matrices of consecutive 16-byte columns
+            const int key = kg * KEYS + n * 8 + (lane & 7);
             const int chunk = ch + (lane >> 3);  // 16-byte column of the key
             uint32_t addr;
             if (C::LINE == 128)
               addr = kt + (chunk >> 3) * (kAtTile * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4);
             else
               addr = kt + key * 64 + ((chunk ^ ((key >> 1) & 3)) << 4);
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(addr, b0, b1, b2, b3);
-            if (FP8) {  // each matrix: 16 columns, this lane's four neighbours = one step
-              mma_16816<true>(sc[n], qf[ch], e4m3x2_to_f16x2(b0), e4m3x2_to_f16x2(b0 >> 16));
-              mma_16816<true>(sc[n], qf[ch + 1], e4m3x2_to_f16x2(b1), e4m3x2_to_f16x2(b1 >> 16));
-              mma_16816<true>(sc[n], qf[ch + 2], e4m3x2_to_f16x2(b2), e4m3x2_to_f16x2(b2 >> 16));
-              mma_16816<true>(sc[n], qf[ch + 3], e4m3x2_to_f16x2(b3), e4m3x2_to_f16x2(b3 >> 16));
-            } else {
-              mma_16816<false>(sc[n], qf[ch / 2], b0, b1);
-              mma_16816<false>(sc[n], qf[ch / 2 + 1], b2, b3);
+            uint32_t (&b)[4] = kb[n];
+            ldsm_x4(addr, b[0], b[1], b[2], b[3]);
+          }
+#pragma unroll
+          for (int m = 0; m < (FP8 ? 4 : 2); ++m) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (FP8)  // each matrix: 16 columns, this lane's four neighbours = one step
+                mma_16816<true>(sc[n], qf[ch + m], e4m3x2_to_f16x2(kb[n][m]), e4m3x2_to_f16x2(kb[n][m] >> 16));
+              else
+                mma_16816<false>(sc[n], qf[ch / 2 + m], kb[n][2 * m], kb[n][2 * m + 1]);
             }
           }
         }
@@ -701,25 +702,46 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         if (sh.last) p.arrived[first] = 0;
       }
       bar_sync_n(1, kAtWarps * 32);
-      if (sh.last && !dead()) {
+      if (sh.last) {
         __threadfence();
-        const int rows_here = min(RB, r_all - blk * RB);
+        const int rows_here = min(RB, r_all - blk * RB), parts = lastb - first + 1;
+        // each row's maximum over the parts: 8 lanes a row
+        float *mrow = reinterpret_cast<float *>(at_smem + 1024 + S * 2 * C::TILE);  // the join buffer
+        for (int r = tid >> 3; r < RB; r += kAtWarps * 4) {
+          float mx = -INFINITY;
+          if (r < rows_here) {
+#pragma unroll 8
+            for (int i = first + (tid & 7); i <= lastb; i += 8) mx = fmaxf(mx, __ldcg(slot_of(i) + RB * D + r));
+          }
+#pragma unroll
+          for (int o2 = 4; o2; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+          if ((tid & 7) == 0) mrow[r] = mx == -INFINITY ? 0.f : mx;
+        }
+        bar_sync_n(1, kAtWarps * 32);
         for (int it = tid; it < rows_here * (D / 4); it += kAtWarps * 32) {
           const int r = it / (D / 4), d4 = it % (D / 4) * 4;
-          float mx = -INFINITY;
-          for (int i = first; i <= lastb; ++i) mx = fmaxf(mx, __ldcg(slot_of(i) + RB * D + r));
-          const float mu = mx == -INFINITY ? 0.f : mx;
+          const float mu = mrow[r];
           float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll 4
-          for (int i = first; i <= lastb; ++i) {
-            const float *w = slot_of(i);
-            const float f = ex2(__ldcg(w + RB * D + r) - mu);
-            const float4 v = ldcg_f4(w + (long long)r * D + d4);
-            l += f * __ldcg(w + RB * D + RB + r);
-            acc[0] += f * v.x;
-            acc[1] += f * v.y;
-            acc[2] += f * v.z;
-            acc[3] += f * v.w;
+          constexpr int U = 12;  // parts in flight
+          for (int i0 = 0; i0 < parts; i0 += U) {
+            float f[U], li[U];
+            float4 v[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const float *w = slot_of(first + min(i0 + k, parts - 1));
+              f[k] = __ldcg(w + RB * D + r);
+              li[k] = __ldcg(w + RB * D + RB + r);
+              v[k] = ldcg_f4(w + (long long)r * D + d4);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const float e = i0 + k < parts ? ex2(f[k] - mu) : 0.f;
+              l += e * li[k];
+              acc[0] += e * v[k].x;
+              acc[1] += e * v[k].y;
+              acc[2] += e * v[k].z;
+              acc[3] += e * v[k].w;
+            }
           }
           const float inv = l > 0.f || l != l ? vs / l : 0.f;
           const int rr = blk * RB + r, t = rr / p.group, head = kv_h * p.group + rr % p.group;
