@@ -22,6 +22,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kvcache.cuh"
 
@@ -32,6 +34,7 @@ constexpr int kAtWarps = 4;      // computing warps
 constexpr int kAtThreads = (kAtWarps + 1) * 32;
 constexpr int kAtStages = 3;
 constexpr int kAtMaxRows = 64;   // rows of a block (MT = 4)
+constexpr float kAtSlack = 8.f;  // log2 of the growth that o is not rescaled for
 
 template <int D, bool FP8>
 struct AttnCfg {
@@ -98,7 +101,8 @@ MOE_HOST_DEV_INLINE bool keys_seen(const SeqView &s, int window, int n_sink, int
 MOE_HOST_DEV_INLINE int tile_at(const SeqTiles &t, int k) { return k < t.lead ? k : k - t.lead + t.first; }
 // Units of a block's run: equal runs over the grid, none shorter than min_units.
 MOE_HOST_DEV_INLINE long long run_length(long long total, long long grid, long long min_units) {
-  const long long run = (total + grid - 1) / grid;
+  const unsigned long long x = total + grid - 1;
+  const long long run = x <= 0xffffffffull ? (unsigned)x / (unsigned)grid : x / grid;
   return run > min_units ? run : min_units;
 }
 
@@ -223,6 +227,10 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const uint32_t stage0 = smem_addr(at_smem) + 1024;
   const uint32_t join = stage0 + S * 2 * C::TILE;
+  if (tid == kAtWarps * 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_addr(&sh.full[i]), 1);
@@ -239,14 +247,21 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   // the thread whose slice contains it.
   const int per = (p.n_seqs + kAtThreads - 1) / kAtThreads;
   const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
-  auto seq_units = [&](int b) {
+  int nt_lo = 0;            // tiles and units of the thread's first sequence
+  long long units_lo = 0;
+  auto seq_units = [&](int b, int &nt) {
     const SeqView s = seq_view(p.row_off, p.kv_len, b, p.n_rows, p.max_pages, p.page);
     if (!s.ok && blockIdx.x == 0) atomicOr(p.status, kErrBadBatch);
     const long long blk = ((long long)s.rows * p.group + RB - 1) / RB;
-    return blk * p.n_kv * seq_tiles(s, p.window, p.n_sink).n;
+    nt = seq_tiles(s, p.window, p.n_sink).n;
+    return blk * p.n_kv * nt;
   };
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(b);
+  if (b_lo < b_hi) units_lo = seq_units(b_lo, nt_lo);
+  long long mine = units_lo;
+  for (int b = b_lo + 1; b < b_hi; ++b) {
+    int nt;
+    mine += seq_units(b, nt);
+  }
   // inclusive scan over the block: within the warps, then over their totals
   long long inc = mine;
 #pragma unroll
@@ -267,19 +282,17 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   const long long u0 = run * blockIdx.x, u1 = min(u0 + run, total);
   if (u0 >= u1) return;  // block-uniform: no work for this block
   if (u0 >= inc - mine && u0 < inc) {
-    long long at = inc - mine;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const long long n = seq_units(b);
-      if (u0 < at + n) {
-        const SeqView s = seq_view(p.row_off, p.kv_len, b, p.n_rows, p.max_pages, p.page);
-        const int nt = seq_tiles(s, p.window, p.n_sink).n;
-        sh.start[0] = b;
-        sh.start[1] = (int)((u0 - at) / nt);
-        sh.start[2] = (int)((u0 - at) % nt);
-        break;
-      }
+    long long at = inc - mine, n = units_lo;
+    int b = b_lo, nt = nt_lo;
+    while (u0 >= at + n) {
       at += n;
+      n = seq_units(++b, nt);
     }
+    const unsigned long long x = u0 - at;
+    const long long seg = x <= 0xffffffffull ? (unsigned)x / (unsigned)nt : x / nt;
+    sh.start[0] = b;
+    sh.start[1] = (int)seg;
+    sh.start[2] = (int)(x - seg * nt);
   }
   __syncthreads();
   AttnCursor c;
@@ -352,6 +365,22 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   // ------------------------------------------------------------ computing
   const int mt = wid % MT, kg = wid / MT;
   const int g = lane >> 2, cq = lane & 3;
+  // where this lane reads in a tile.  Keys: row 8 n + lane % 8, 16-byte column
+  // 4 i + lane / 8 of a line; values: row 16 ks + lane % 16, column 2 i + lane /
+  // 16; the swizzle turns a column's number by the row's (mod 8, or mod 4 of
+  // row / 2 in 64-byte lines).
+  constexpr int KOFF = C::LINE / 64, VOFF = C::LINE / 32;
+  uint32_t koff[KOFF], voff[VOFF];
+#pragma unroll
+  for (int i = 0; i < KOFF; ++i) {
+    const int key = kg * KEYS + (lane & 7), x = C::LINE == 128 ? key & 7 : (key >> 1) & 3;
+    koff[i] = key * C::LINE + (((4 * i + (lane >> 3)) ^ x) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < VOFF; ++i) {
+    const int key = kg * KEYS + (lane & 15), x = C::LINE == 128 ? key & 7 : (key >> 1) & 3;
+    voff[i] = key * C::LINE + (((2 * i + (lane >> 4)) ^ x) << 4);
+  }
   long long n_done = 0;
   long long u = u0;
   bool live = true;  // false once a wait of this warp gave up: it goes on through the shared barriers
@@ -416,8 +445,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e of the largest element, kept where 2^-e is a normal number
-        const uint32_t e = min(max(top >> 23, 1u), 253u);
+        // 2^e of the largest element (at least 2^-63: a row of zeros keeps a
+        // scale above zero), kept where 2^-e is a normal number
+        const uint32_t e = min(max(top >> 23, 64u), 253u);
         const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
         row_scale[i] *= ks * up;
 #pragma unroll
@@ -455,13 +485,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             // four 8-key x 16-byte matrices of consecutive 16-byte columns
-            const int key = kg * KEYS + n * 8 + (lane & 7);
-            const int chunk = ch + (lane >> 3);  // 16-byte column of the key
-            uint32_t addr;
-            if (C::LINE == 128)
-              addr = kt + (chunk >> 3) * (kAtTile * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4);
-            else
-              addr = kt + key * 64 + ((chunk ^ ((key >> 1) & 3)) << 4);
+            const uint32_t addr = kt + koff[ch % (4 * KOFF) / 4] + ch / (4 * KOFF) * (kAtTile * C::LINE) +
+                                  n * 8 * C::LINE;
             uint32_t (&b)[4] = kb[n];
             ldsm_x4(addr, b[0], b[1], b[2], b[3]);
           }
@@ -480,10 +505,6 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         const int tile0 = tile * kAtTile, last = tile0 + kAtTile - 1;
         const int pos1 = c.s.kv - 1;
         const bool whole = last <= pos0 && (p.window <= 0 || pos1 - tile0 < p.window || last < p.n_sink);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][e] *= row_scale[e >> 1];
         if (!whole) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -494,25 +515,31 @@ __global__ void __launch_bounds__(kAtThreads, 2)
               if (!seen) sc[n][e] = -INFINITY;
             }
         }
-        // ---- running maximum and sum
-        float corr[2], m_use[2];
+        // ---- running maximum and sum.  The terms are scaled by a reference
+        // that follows the maximum only when it fell kAtSlack behind (p then
+        // holds values up to 2^kAtSlack): o is rarely rescaled
+        float corr[2] = {1.f, 1.f}, neg[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float mx = m_run[i];
+          float mx = -INFINITY;
 #pragma unroll
           for (int n = 0; n < NT; ++n) mx = fmaxf(mx, fmaxf(sc[n][2 * i], sc[n][2 * i + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          m_use[i] = mx == -INFINITY ? 0.f : mx;  // nothing seen yet: every p below is 2^-inf = 0
-          corr[i] = ex2(m_run[i] - m_use[i]);
-          m_run[i] = mx;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * row_scale[i];
+          if (m_run[i] == -INFINITY) {
+            m_run[i] = mx;
+          } else if (mx > m_run[i] + kAtSlack) {
+            corr[i] = ex2(m_run[i] - mx);
+            m_run[i] = mx;
+          }
+          neg[i] = m_run[i] == -INFINITY ? 0.f : -m_run[i];  // nothing seen yet: every p below is 2^-inf = 0
         }
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[n][e] = ex2(sc[n][e] - m_use[e >> 1]);
+            sc[n][e] = ex2(__fmaf_rn(sc[n][e], row_scale[e >> 1], neg[e >> 1]));
             sum[e >> 1] += sc[n][e];
           }
         l_run[0] = l_run[0] * corr[0] + sum[0];
@@ -529,63 +556,57 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         // ---- o += p v.  p is rounded to the tensor cores' 16 bits (at most
         // half a step of each term); values no row of the call sees may hold
         // anything, infinities and NaN included, and are read as zeros.
-        const int seen_end = c.s.kv;                           // keys from here on do not exist
-        const int hid0 = p.window > 0 ? p.n_sink : 0x7fffffff; // [hid0, hid1) lies before every window
-        const long long hid1 = (long long)pos0 - p.window + 1;
+        auto values = [&](auto edge_tile) {
+          constexpr bool EDGE = decltype(edge_tile)::value;
+          const int seen_end = c.s.kv;                           // keys from here on do not exist
+          const int hid0 = p.window > 0 ? p.n_sink : 0x7fffffff; // [hid0, hid1) lies before every window
+          const long long hid1 = (long long)pos0 - p.window + 1;
 #pragma unroll
-        for (int ks = 0; ks < KEYS / 16; ++ks) {
-          uint32_t a[4];
-          if (FP8) {
-            a[0] = pack_f16(sc[2 * ks][0], sc[2 * ks][1]);
-            a[1] = pack_f16(sc[2 * ks][2], sc[2 * ks][3]);
-            a[2] = pack_f16(sc[2 * ks + 1][0], sc[2 * ks + 1][1]);
-            a[3] = pack_f16(sc[2 * ks + 1][2], sc[2 * ks + 1][3]);
-          } else {
-            a[0] = pack_bf16(sc[2 * ks][0], sc[2 * ks][1]);
-            a[1] = pack_bf16(sc[2 * ks][2], sc[2 * ks][3]);
-            a[2] = pack_bf16(sc[2 * ks + 1][0], sc[2 * ks + 1][1]);
-            a[3] = pack_bf16(sc[2 * ks + 1][2], sc[2 * ks + 1][3]);
-          }
-          // the keys of this lane's fragment registers: j, j+1 and j+8, j+9
-          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-          if (!whole) {
-            keep0 = keep1 = 0;
+          for (int ks = 0; ks < KEYS / 16; ++ks) {
+            uint32_t a[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = key0 + ks * 16 + 2 * cq + (e & 1) + 8 * (e >> 1);
-              const bool keep = j < seen_end && !(j >= hid0 && j < hid1);
-              const uint32_t bits = keep ? ((e & 1) ? 0xffff0000u : 0x0000ffffu) : 0u;
-              if (e < 2) keep0 |= bits;
-              else keep1 |= bits;
+            for (int i = 0; i < 4; ++i) {
+              const float lo = sc[2 * ks + (i >> 1)][(i & 1) * 2], hi = sc[2 * ks + (i >> 1)][(i & 1) * 2 + 1];
+              a[i] = FP8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+            }
+            // the keys of this lane's fragment registers: j, j+1 and j+8, j+9
+            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+            if (EDGE) {
+              keep0 = keep1 = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int j = key0 + ks * 16 + 2 * cq + (e & 1) + 8 * (e >> 1);
+                const bool keep = j < seen_end && !(j >= hid0 && j < hid1);
+                const uint32_t bits = keep ? ((e & 1) ? 0xffff0000u : 0x0000ffffu) : 0u;
+                if (e < 2) keep0 |= bits;
+                else keep1 |= bits;
+              }
+            }
+            auto k0 = [&](uint32_t v) { return EDGE ? v & keep0 : v; };
+            auto k1 = [&](uint32_t v) { return EDGE ? v & keep1 : v; };
+#pragma unroll
+            for (int ch = 0; ch < C::ROWB / 16; ch += 2) {
+              const uint32_t addr = vt + voff[ch % (2 * VOFF) / 2] + ch / (2 * VOFF) * (kAtTile * C::LINE) +
+                                    ks * 16 * C::LINE;
+              uint32_t b0, b1, b2, b3;
+              ldsm_x4_t(addr, b0, b1, b2, b3);
+              if (FP8) {
+                // bytes of a register: key j: columns 2g, 2g+1; key j+1: the same
+                const uint32_t x0 = __byte_perm(b0, 0, 0x3120), x1 = __byte_perm(b1, 0, 0x3120);
+                const uint32_t x2 = __byte_perm(b2, 0, 0x3120), x3 = __byte_perm(b3, 0, 0x3120);
+                mma_16816<true>(o[2 * ch], a, k0(e4m3x2_to_f16x2(x0)), k1(e4m3x2_to_f16x2(x1)));
+                mma_16816<true>(o[2 * ch + 1], a, k0(e4m3x2_to_f16x2(x0 >> 16)), k1(e4m3x2_to_f16x2(x1 >> 16)));
+                mma_16816<true>(o[2 * ch + 2], a, k0(e4m3x2_to_f16x2(x2)), k1(e4m3x2_to_f16x2(x3)));
+                mma_16816<true>(o[2 * ch + 3], a, k0(e4m3x2_to_f16x2(x2 >> 16)), k1(e4m3x2_to_f16x2(x3 >> 16)));
+              } else {
+                mma_16816<false>(o[ch], a, k0(b0), k1(b1));
+                mma_16816<false>(o[ch + 1], a, k0(b2), k1(b3));
+              }
             }
           }
-          const int key = kg * KEYS + ks * 16 + (lane & 15);
-#pragma unroll
-          for (int ch = 0; ch < C::ROWB / 16; ch += 2) {
-            const int chunk = ch + (lane >> 4);
-            uint32_t addr;
-            if (C::LINE == 128)
-              addr = vt + (chunk >> 3) * (kAtTile * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4);
-            else
-              addr = vt + key * 64 + ((chunk ^ ((key >> 1) & 3)) << 4);
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(addr, b0, b1, b2, b3);
-            if (FP8) {
-              // bytes of a register: key j: columns 2g, 2g+1; key j+1: the same
-              const uint32_t x0 = __byte_perm(b0, 0, 0x3120), x1 = __byte_perm(b1, 0, 0x3120);
-              const uint32_t x2 = __byte_perm(b2, 0, 0x3120), x3 = __byte_perm(b3, 0, 0x3120);
-              mma_16816<true>(o[2 * ch], a, e4m3x2_to_f16x2(x0) & keep0, e4m3x2_to_f16x2(x1) & keep1);
-              mma_16816<true>(o[2 * ch + 1], a, e4m3x2_to_f16x2(x0 >> 16) & keep0,
-                              e4m3x2_to_f16x2(x1 >> 16) & keep1);
-              mma_16816<true>(o[2 * ch + 2], a, e4m3x2_to_f16x2(x2) & keep0, e4m3x2_to_f16x2(x3) & keep1);
-              mma_16816<true>(o[2 * ch + 3], a, e4m3x2_to_f16x2(x2 >> 16) & keep0,
-                              e4m3x2_to_f16x2(x3 >> 16) & keep1);
-            } else {
-              mma_16816<false>(o[ch], a, b0 & keep0, b1 & keep1);
-              mma_16816<false>(o[ch + 1], a, b2 & keep0, b3 & keep1);
-            }
-          }
-        }
+        };
+        if (whole) values(std::false_type{});
+        else values(std::true_type{});
       } else if (lane == 0 && !dead()) {
         give_up();
       }
@@ -693,61 +714,104 @@ __global__ void __launch_bounds__(kAtThreads, 2)
             w[RB * D + RB + r] = l_run[i];
           }
         }
-        __threadfence();
       }
       bar_sync_n(1, kAtWarps * 32);
       if (tid == 0) {
         const unsigned int parts = lastb - first + 1;
+        __threadfence();  // the block's part before its arrival, and every part before the join
         sh.last = atomicAdd(p.arrived + first, 1u) == parts - 1;
         if (sh.last) p.arrived[first] = 0;
+        __threadfence();
       }
       bar_sync_n(1, kAtWarps * 32);
       if (sh.last) {
-        __threadfence();
         const int rows_here = min(RB, r_all - blk * RB), parts = lastb - first + 1;
-        // each row's maximum over the parts: 8 lanes a row
-        float *mrow = reinterpret_cast<float *>(at_smem + 1024 + S * 2 * C::TILE);  // the join buffer
-        for (int r = tid >> 3; r < RB; r += kAtWarps * 4) {
-          float mx = -INFINITY;
-          if (r < rows_here) {
-#pragma unroll 8
-            for (int i = first + (tid & 7); i <= lastb; i += 8) mx = fmaxf(mx, __ldcg(slot_of(i) + RB * D + r));
-          }
-#pragma unroll
-          for (int o2 = 4; o2; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-          if ((tid & 7) == 0) mrow[r] = mx == -INFINITY ? 0.f : mx;
-        }
-        bar_sync_n(1, kAtWarps * 32);
-        for (int it = tid; it < rows_here * (D / 4); it += kAtWarps * 32) {
-          const int r = it / (D / 4), d4 = it % (D / 4) * 4;
-          const float mu = mrow[r];
-          float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-          constexpr int U = 12;  // parts in flight
-          for (int i0 = 0; i0 < parts; i0 += U) {
+        auto store = [&](int r, int d4, const float (&acc)[4], float inv) {
+          const int rr = blk * RB + r, t = rr / p.group, head = kv_h * p.group + rr % p.group;
+          uint16_t *dst = p.out + (long long)(c.s.row0 + t) * p.out_stride + (long long)head * D + d4;
+          *reinterpret_cast<uint2 *>(dst) =
+              make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        };
+        constexpr int U = 8;  // parts in flight
+        if (parts <= U) {
+          for (int it = tid; it < rows_here * (D / 4); it += kAtWarps * 32) {
+            const int r = it / (D / 4), d4 = it % (D / 4) * 4;
             float f[U], li[U];
             float4 v[U];
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-              const float *w = slot_of(first + min(i0 + k, parts - 1));
+              const float *w = slot_of(first + min(k, parts - 1));
               f[k] = __ldcg(w + RB * D + r);
               li[k] = __ldcg(w + RB * D + RB + r);
               v[k] = ldcg_f4(w + (long long)r * D + d4);
             }
+            float mx = f[0];
+#pragma unroll
+            for (int k = 1; k < U; ++k) mx = fmaxf(mx, f[k]);
+            const float mu = mx == -INFINITY ? 0.f : mx;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-              const float e = i0 + k < parts ? ex2(f[k] - mu) : 0.f;
+              const float e = k < parts ? ex2(f[k] - mu) : 0.f;
               l += e * li[k];
               acc[0] += e * v[k].x;
               acc[1] += e * v[k].y;
               acc[2] += e * v[k].z;
               acc[3] += e * v[k].w;
             }
+            store(r, d4, acc, l > 0.f || l != l ? vs / l : 0.f);
           }
-          const float inv = l > 0.f || l != l ? vs / l : 0.f;
-          const int rr = blk * RB + r, t = rr / p.group, head = kv_h * p.group + rr % p.group;
-          uint16_t *dst = p.out + (long long)(c.s.row0 + t) * p.out_stride + (long long)head * D + d4;
-          *reinterpret_cast<uint2 *>(dst) =
-              make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        } else {
+          // Each part's weight first, a warp per row (as many rows at once as
+          // the join buffer holds weights for), then the weighted sums.
+          float *wgt = reinterpret_cast<float *>(at_smem + 1024 + S * 2 * C::TILE);
+          float *inv = &sh.ml[0][0][0][0];  // of up to 64 rows
+          const int at_once = min(rows_here, (int)(C::JOIN / sizeof(float)) / parts);
+          for (int r0 = 0; r0 < rows_here; r0 += at_once) {
+            const int nr = min(at_once, rows_here - r0);
+            for (int r = wid; r < nr; r += kAtWarps) {
+              float mx = -INFINITY, l = 0.f;
+#pragma unroll 4
+              for (int i = lane; i < parts; i += 32) {
+                const float m = __ldcg(slot_of(first + i) + RB * D + r0 + r);
+                wgt[r * parts + i] = m;
+                mx = fmaxf(mx, m);
+              }
+#pragma unroll
+              for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+              const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
+              for (int i = lane; i < parts; i += 32) {
+                const float e = ex2(wgt[r * parts + i] - mu);
+                wgt[r * parts + i] = e;
+                l += e * __ldcg(slot_of(first + i) + RB * D + RB + r0 + r);
+              }
+              l = warp_sum(l);
+              if (lane == 0) inv[r] = l > 0.f || l != l ? vs / l : 0.f;
+            }
+            bar_sync_n(1, kAtWarps * 32);
+            for (int it = tid; it < nr * (D / 4); it += kAtWarps * 32) {
+              const int r = it / (D / 4), d4 = it % (D / 4) * 4;
+              const long long at = (long long)(r0 + r) * D + d4;
+              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+              constexpr int W = 16;
+              for (int i0 = 0; i0 < parts; i0 += W) {
+                float4 v[W];
+#pragma unroll
+                for (int k = 0; k < W; ++k) v[k] = ldcg_f4(slot_of(first + min(i0 + k, parts - 1)) + at);
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                  const float e = i0 + k < parts ? wgt[r * parts + i0 + k] : 0.f;
+                  acc[0] += e * v[k].x;
+                  acc[1] += e * v[k].y;
+                  acc[2] += e * v[k].z;
+                  acc[3] += e * v[k].w;
+                }
+              }
+              store(r0 + r, d4, acc, inv[r]);
+            }
+            bar_sync_n(1, kAtWarps * 32);  // the weights have been read
+          }
         }
       }
       bar_sync_n(1, kAtWarps * 32);  // sh.last is read before the next segment writes it

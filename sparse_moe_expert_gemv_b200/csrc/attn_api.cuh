@@ -247,7 +247,7 @@ moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_st
   p.page = a.page;
   p.page_shift = 0;
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
-  p.min_units = 1;
+  p.min_units = 4;
   p.ws = a.ws;
   p.arrived = a.arrived;
   p.status = a.status;
