@@ -316,8 +316,10 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     const int my_col = lane / 2 % C::NB;       // column box, keys or values
     const bool my_v = lane & 1;
     int held_b = -1, held_at = 0, held = 0;    // 32 entries of the page table, one per lane
-    long long issued = 0;
-    for (long long u = u0; u < u1 && !dead(); ++u, ++issued) {
+    int st = 0;
+    uint32_t phase = 1;   // a new barrier passes the wait for its preceding phase
+    long long u = u0;
+    for (; u < u1 && !dead(); ++u) {
       const int tile = tile_at(c.t, c.k);
       const int key0 = tile * kAtTile;
       const int blk_h = c.seg / c.nblk;
@@ -329,10 +331,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         const int i = pg0 + lane;
         held = i < n_pg ? __ldg(p.page_table + (long long)c.b * p.max_pages + i) : 0;
       }
-      const int st = (int)(issued % S);
-      const uint32_t use = (uint32_t)(issued / S);
       const uint32_t bar = smem_addr(&sh.full[st]);
-      if (use > 0 && !mbar_wait_warp(smem_addr(&sh.empty[st]), (use - 1) & 1, &sh.dead)) {
+      if (!mbar_wait_warp(smem_addr(&sh.empty[st]), phase, &sh.dead)) {
         if (lane == 0) give_up();
         break;
       }
@@ -355,10 +355,14 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         tma_box_2d(dst, my_v ? &vmap : &kmap, my_col * (FP8 ? 128 : 64), y, bar, policy);
       }
       if (++c.k == c.t.n) cursor_next_seg<RB>(c, p);
+      if (++st == S) st = 0, phase ^= 1;
     }
-    // no tile may land after the block has gone
-    for (long long i = max(0LL, issued - S); i < issued; ++i)
-      (void)mbar_wait_bounded(smem_addr(&sh.full[i % S]), (uint32_t)(i / S) & 1);
+    // no tile may land after the block has gone: each stage's last use
+    const long long issued = u - u0;
+    for (int i = 0; i < S && i < issued; ++i) {
+      const uint32_t uses = (uint32_t)((issued - 1 - i) / S);
+      (void)mbar_wait_bounded(smem_addr(&sh.full[i]), uses & 1);
+    }
     return;
   }
 
@@ -381,7 +385,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     const int key = kg * KEYS + (lane & 15), x = C::LINE == 128 ? key & 7 : (key >> 1) & 3;
     voff[i] = key * C::LINE + (((2 * i + (lane >> 4)) ^ x) << 4);
   }
-  long long n_done = 0;
+  int st = 0;            // the ring's stage and the parity of its present use
+  uint32_t phase = 0;
   long long u = u0;
   bool live = true;  // false once a wait of this warp gave up: it goes on through the shared barriers
   while (u < u1) {
@@ -466,10 +471,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     for (int n = 0; n < ND; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
-    for (int k = k_beg; k < k_end; ++k, ++n_done) {
-      const int st = (int)(n_done % S);
-      const uint32_t use = (uint32_t)(n_done / S);
-      live = live && mbar_wait_warp(smem_addr(&sh.full[st]), use & 1, &sh.dead);
+    for (int k = k_beg; k < k_end; ++k) {
+      live = live && mbar_wait_live(smem_addr(&sh.full[st]), phase, &sh.dead);
+      live = __all_sync(0xffffffffu, live);
       if (live) {
         const int tile = tile_at(c.t, k);
         const int key0 = tile * kAtTile + kg * KEYS;  // first key of this warp
@@ -612,6 +616,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
+      if (++st == S) st = 0, phase ^= 1;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // the four lanes of a row hold parts of its sum
