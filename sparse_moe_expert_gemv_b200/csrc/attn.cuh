@@ -242,64 +242,140 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   __syncthreads();
   pdl_wait();
 
-  // ---- the list of units: its length, and where this block's run begins.
-  // Every thread holds a slice of the sequences; the runs' start is found by
-  // the thread whose slice contains it.
-  const int per = (p.n_seqs + kAtThreads - 1) / kAtThreads;
-  const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
-  int nt_lo = 0;            // tiles and units of the thread's first sequence
-  long long units_lo = 0;
-  auto seq_units = [&](int b, int &nt) {
+  // ---- the list of units: its length, and where this block's run begins
+  auto units_of = [&](const SeqView &s, const SeqTiles &t) {
+    return (((long long)s.rows * p.group + RB - 1) / RB) * p.n_kv * t.n;
+  };
+  auto view = [&](int b) {
     const SeqView s = seq_view(p.row_off, p.kv_len, b, p.n_rows, p.max_pages, p.page);
     if (!s.ok && blockIdx.x == 0) atomicOr(p.status, kErrBadBatch);
-    const long long blk = ((long long)s.rows * p.group + RB - 1) / RB;
-    nt = seq_tiles(s, p.window, p.n_sink).n;
-    return blk * p.n_kv * nt;
+    return s;
   };
-  if (b_lo < b_hi) units_lo = seq_units(b_lo, nt_lo);
-  long long mine = units_lo;
-  for (int b = b_lo + 1; b < b_hi; ++b) {
-    int nt;
-    mine += seq_units(b, nt);
-  }
-  // inclusive scan over the block: within the warps, then over their totals
-  long long inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) sh.scan[wid] = inc;
-  __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kAtWarps + 1; ++w) {
-    if (w < wid) before += sh.scan[w];
-    total += sh.scan[w];
-  }
-  inc += before;
-  const long long run = run_length(total, gridDim.x, p.min_units);
-  const long long u0 = run * blockIdx.x, u1 = min(u0 + run, total);
-  if (u0 >= u1) return;  // block-uniform: no work for this block
-  if (u0 >= inc - mine && u0 < inc) {
-    long long at = inc - mine, n = units_lo;
-    int b = b_lo, nt = nt_lo;
-    while (u0 >= at + n) {
-      at += n;
-      n = seq_units(++b, nt);
-    }
-    const unsigned long long x = u0 - at;
-    const long long seg = x <= 0xffffffffull ? (unsigned)x / (unsigned)nt : x / nt;
-    sh.start[0] = b;
-    sh.start[1] = (int)seg;
-    sh.start[2] = (int)(x - seg * nt);
-  }
-  __syncthreads();
   AttnCursor c;
-  c.b = sh.start[0];
-  cursor_load<RB>(c, p);
-  c.seg = sh.start[1];
-  c.k = sh.start[2];
+  long long total, run, u0, u1;
+  bool own = false;  // each block belongs to one segment: its blocks are
+  int own_first = 0, own_last = 0;
+  auto cut = [&] {
+    run = run_length(total, gridDim.x, p.min_units);
+    u0 = run * blockIdx.x;
+    u1 = min(u0 + run, total);
+  };
+  auto place = [&](unsigned long long x, int nt, int &seg, int &k) {  // unit x of a sequence
+    const long long q = x <= 0xffffffffull ? (unsigned)x / (unsigned)nt : x / nt;
+    seg = (int)q;
+    k = (int)(x - q * nt);
+  };
+  if (p.n_seqs <= 32) {
+    // few sequences: every warp finds the place for itself, a lane per sequence
+    SeqView s{0, 0, 0, true};
+    SeqTiles t{0, 0, 0};
+    if (lane < p.n_seqs) {
+      s = view(lane);
+      t = seq_tiles(s, p.window, p.n_sink);
+    }
+    const long long units = units_of(s, t);
+    total = units;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    run = run_length(total, gridDim.x, p.min_units);
+    // Where a slightly longer run lets every segment have blocks of its own,
+    // no block has two parts to hand over.
+    const int segs = t.n ? (int)(units / t.n) : 0;
+    int need = 0;
+    if (total <= 0x7fffffff) {
+      const int most = (int)run + ((int)run + 3) / 4;
+      for (int r = (int)run; r <= most && !own; ++r) {
+        need = __reduce_add_sync(0xffffffffu, segs * ((t.n + r - 1) / r));
+        if (need <= (int)gridDim.x) own = true, run = r;
+      }
+    }
+    const long long mine = own ? segs * ((t.n + (int)run - 1) / (int)run) : units;  // blocks, or units
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    u0 = own ? blockIdx.x : run * blockIdx.x;
+    if (u0 >= (own ? need : total)) return;  // block-uniform: no work for this block
+    const int f = __ffs(__ballot_sync(0xffffffffu, u0 < inc)) - 1;
+    const long long x = u0 - __shfl_sync(0xffffffffu, inc - mine, f);  // within sequence f
+    c.b = f;
+    c.s.row0 = __shfl_sync(0xffffffffu, s.row0, f);
+    c.s.rows = __shfl_sync(0xffffffffu, s.rows, f);
+    c.s.kv = __shfl_sync(0xffffffffu, s.kv, f);
+    c.s.ok = true;
+    c.t.lead = __shfl_sync(0xffffffffu, t.lead, f);
+    c.t.first = __shfl_sync(0xffffffffu, t.first, f);
+    c.t.n = __shfl_sync(0xffffffffu, t.n, f);
+    c.nblk = (c.s.rows * p.group + RB - 1) / RB;
+    if (own) {
+      const int parts = (c.t.n + (int)run - 1) / (int)run;
+      int part;
+      place(x, parts, c.seg, part);
+      own_first = blockIdx.x - part;
+      own_last = own_first + parts - 1;
+      c.k = part * (int)run;
+      u0 = 0;
+      u1 = min((int)run, c.t.n - c.k);
+    } else {
+      place(x, c.t.n, c.seg, c.k);
+      u1 = min(u0 + run, total);
+    }
+  } else {
+    // every thread holds a slice of the sequences; the thread whose slice
+    // holds the place tells the others
+    const int per = (p.n_seqs + kAtThreads - 1) / kAtThreads;
+    const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
+    auto seq_units = [&](int b, int &nt) {
+      const SeqView s = view(b);
+      const SeqTiles t = seq_tiles(s, p.window, p.n_sink);
+      nt = t.n;
+      return units_of(s, t);
+    };
+    int nt_lo = 0;  // tiles and units of the thread's first sequence
+    long long units_lo = 0;
+    if (b_lo < b_hi) units_lo = seq_units(b_lo, nt_lo);
+    long long mine = units_lo;
+    for (int b = b_lo + 1; b < b_hi; ++b) {
+      int nt;
+      mine += seq_units(b, nt);
+    }
+    // inclusive scan over the block: within the warps, then over their totals
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sh.scan[wid] = inc;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kAtWarps + 1; ++w) {
+      if (w < wid) before += sh.scan[w];
+      total += sh.scan[w];
+    }
+    inc += before;
+    cut();
+    if (u0 >= u1) return;  // block-uniform: no work for this block
+    if (u0 >= inc - mine && u0 < inc) {
+      long long at = inc - mine, n = units_lo;
+      int b = b_lo, nt = nt_lo;
+      while (u0 >= at + n) {
+        at += n;
+        n = seq_units(++b, nt);
+      }
+      sh.start[0] = b;
+      place(u0 - at, nt, sh.start[1], sh.start[2]);
+    }
+    __syncthreads();
+    c.b = sh.start[0];
+    cursor_load<RB>(c, p);
+    c.seg = sh.start[1];
+    c.k = sh.start[2];
+  }
   auto dead = [&]() { return *reinterpret_cast<volatile int *>(&sh.dead) != 0; };
   auto give_up = [&]() {
     *reinterpret_cast<volatile int *>(&sh.dead) = 1;
@@ -700,7 +776,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       // the segment's first block wrote slot 1 (its run ends inside it), the
       // others slot 0 (their run begins inside it)
       const long long seg_u0 = u - k_beg, seg_u1 = seg_u0 + c.t.n;
-      const int first = (int)(seg_u0 / run), lastb = (int)((seg_u1 - 1) / run);
+      const int first = own ? own_first : (int)(seg_u0 / run);
+      const int lastb = own ? own_last : (int)((seg_u1 - 1) / run);
       auto slot_of = [&](int blk_id) {
         return p.ws + ((long long)blk_id * 2 + (blk_id == first ? 1 : 0)) * (RB * (D + 2));
       };

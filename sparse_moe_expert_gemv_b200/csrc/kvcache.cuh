@@ -9,10 +9,12 @@
 // to 0.06 rad.
 //
 // What bounds it: one read and one write of every row (plus launch latency
-// for a window's few rows).  A block takes `rows_per_block` rows, computes
+// for a window's few rows).  A block takes ROWS rows, computes
 // their rotations once in shared memory for all heads, and streams the heads
 // with D / 8 lanes each, two 8-byte (four-element) pieces per lane placed so
-// that both elements of a pair sit in the same lane.
+// that both elements of a pair sit in the same lane.  A warp stays with one
+// row: dealing head rows out across rows cost more in index arithmetic than
+// the arithmetic itself.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -22,7 +24,7 @@
 namespace moe {
 
 constexpr int kKvThreads = 256;
-constexpr int kKvMaxRows = 4;   // rows per block
+constexpr int kKvRows = 8;      // rows of a block once there are enough of them
 constexpr int kKvMaxDim = 128;
 
 // A sequence's rows in the call and its cache length, checked: the offsets
@@ -59,7 +61,7 @@ struct KvRowsParams {
   int norm;
   const double *inv_freq;             // [rot / 2] or null
   int rot, interleaved;
-  int n_rows, n_q, n_kv, rows_per_block;
+  int n_rows, n_q, n_kv;
   // cache
   uint8_t *k_cache, *v_cache;         // [n_pages][n_kv][page][D]
   const float *k_scale, *v_scale;     // e4m3: [n_kv] or null
@@ -92,27 +94,29 @@ MOE_DEV uint32_t float_to_e4m3x4(const float *x) {
 
 // CACHE 0: q and k rows to q_out and k_out; 1: q rows to q_out (when given),
 // k and v rows to a bf16 cache; 2: the same with an e4m3 cache.
-template <int D, int CACHE>
+template <int D, int CACHE, int ROWS>
 __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
-  constexpr int LPH = D / 8;  // lanes of a head row
-  constexpr int PRE = 3;      // head rows in flight per lane
-  __shared__ float2 s_cs[kKvMaxRows][kKvMaxDim / 2];
-  __shared__ int s_seq[kKvMaxRows];   // sequences that end at or before the row
-  __shared__ int s_pos[kKvMaxRows];
-  __shared__ long long s_at[kKvMaxRows];  // cache row of KV head 0, or -1
-  const int tid = threadIdx.x;
-  const int r0 = blockIdx.x * p.rows_per_block;
-  const int nr = min(p.rows_per_block, p.n_rows - r0);
-  if (tid < kKvMaxRows) s_seq[tid] = 0;
+  constexpr int LPH = D / 8;    // lanes of a head row
+  constexpr int HPW = 32 / LPH; // head rows of a warp's step
+  constexpr int NW = kKvThreads / 32;
+  __shared__ __align__(16) float2 s_cs[ROWS][kKvMaxDim / 2];
+  __shared__ int s_seq[ROWS];   // sequences that end at or before the row
+  __shared__ int s_pos[ROWS];
+  __shared__ long long s_at[ROWS];  // cache row of KV head 0, or -1
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int r0 = blockIdx.x * ROWS;
+  const int nr = min(ROWS, p.n_rows - r0);
+  if (CACHE && tid < ROWS) s_seq[tid] = 0;
   pdl_wait();
 
+  // A row's heads are shared by NW / ROWS warps, HPW at a time; a
+  // warp stays with its row, whose rotation it holds in registers.
   const int heads = p.n_q + p.n_kv * (CACHE ? 2 : 1);
-  const int hq0 = (CACHE && p.q == nullptr) ? p.n_q : 0;  // first head of the call
-  const int per_row = heads - hq0;
-  const int total = nr * per_row;
-  const int group = tid / LPH, sub = tid % LPH;
-  const uint32_t group_mask = ((1u << LPH) - 1u) << ((tid & 31) / LPH * LPH);  // the lanes of one head row
-  constexpr int NG = kKvThreads / LPH;
+  const int h_first = (CACHE && p.q == nullptr) ? p.n_q : 0;  // first head of the call
+  const int parts = NW / ROWS;
+  const int r = wid / parts, part = wid % parts, sub = lane % LPH;
+  const long long row = r0 + r;
+  const bool mine = r < nr;
   // the lane's two pieces of a head row: four first and four second elements
   // of rotated pairs, or eight neighbours
   int e0, e1;
@@ -125,33 +129,34 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
     e0 = 8 * sub;
     e1 = e0 + 4;
   }
-  auto load = [&](int item, uint2 &a, uint2 &b) {
-    const int r = item / per_row, h = hq0 + item - r * per_row;
-    const uint16_t *src;
-    const long long row = r0 + r;
-    if (h < p.n_q) src = p.q + row * p.q_stride + (long long)h * D;
-    else if (h < p.n_q + p.n_kv) src = p.k + row * p.k_stride + (long long)(h - p.n_q) * D;
-    else src = p.v + row * p.v_stride + (long long)(h - p.n_q - p.n_kv) * D;
+  const int step = parts * HPW;
+  int h = h_first + part * HPW + lane / LPH;
+  const uint16_t *q_row = p.q + row * p.q_stride, *k_row = p.k + row * p.k_stride - (long long)p.n_q * D;
+  const uint16_t *v_row = CACHE ? p.v + row * p.v_stride - (long long)(p.n_q + p.n_kv) * D : nullptr;
+  auto load = [&](int h, uint2 &a, uint2 &b) {
+    const uint16_t *src = h < p.n_q ? q_row : CACHE && h >= p.n_q + p.n_kv ? v_row : k_row;
+    src += (long long)h * D;
     a = *reinterpret_cast<const uint2 *>(src + e0);
     b = *reinterpret_cast<const uint2 *>(src + e1);
   };
-  // the first rows are on their way while the positions are looked up
+  // the first heads are on their way while the positions are looked up
+  constexpr int PRE = 2;
   uint2 xa[PRE], xb[PRE];
 #pragma unroll
   for (int i = 0; i < PRE; ++i)
-    if (group + i * NG < total) load(group + i * NG, xa[i], xb[i]);
+    if (mine && h + i * step < heads) load(h + i * step, xa[i], xb[i]);
 
   if (CACHE) {
     // each row's sequence: the number of sequences that end at or before it
-    int cnt[kKvMaxRows] = {};
+    int cnt[ROWS] = {};
     __syncthreads();
     for (int b = tid; b < p.n_seqs; b += kKvThreads) {
       const int end = __ldg(p.row_off + b + 1);
 #pragma unroll
-      for (int r = 0; r < kKvMaxRows; ++r) cnt[r] += end <= r0 + r;
+      for (int r = 0; r < ROWS; ++r) cnt[r] += end <= r0 + r;
     }
 #pragma unroll
-    for (int r = 0; r < kKvMaxRows; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       const int c = __reduce_add_sync(0xffffffffu, cnt[r]);
       if ((tid & 31) == 0 && c) atomicAdd(&s_seq[r], c);
     }
@@ -192,9 +197,22 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
     __syncthreads();
   }
 
-  auto finish = [&](int item, uint2 a, uint2 b) {
-    const int r = item / per_row, h = hq0 + item - r * per_row;
-    const bool is_q = h < p.n_q, is_v = h >= p.n_q + p.n_kv;
+  if (!mine) return;
+  const int pos = s_pos[r];
+  if (CACHE && pos < 0) return;  // a row of no sequence: left as it was
+  const long long at = CACHE ? s_at[r] : 0;
+  float co[4], si[4];
+  if (turns) {
+    const float4 *cs = reinterpret_cast<const float4 *>(&s_cs[r][4 * sub]);  // (cos, sin) of two pairs each
+    const float4 c01 = cs[0], c23 = cs[1];
+    co[0] = c01.x, co[1] = c01.z, co[2] = c23.x, co[3] = c23.z;
+    si[0] = c01.y, si[1] = c01.w, si[2] = c23.y, si[3] = c23.w;
+  }
+  uint16_t *qo_row = p.q_out + row * p.q_out_stride;
+  uint16_t *ko_row = CACHE ? nullptr : p.k_out + row * p.k_out_stride - (long long)p.n_q * D;
+  const uint32_t lanes = ((1u << LPH) - 1u) << (lane / LPH * LPH);  // the lanes of one head row
+  auto finish = [&](int h, uint2 a, uint2 b) {
+    const bool is_q = h < p.n_q, is_v = CACHE && h >= p.n_q + p.n_kv;
     float x[8];
     bf16x4_to_float(a, x);
     bf16x4_to_float(b, x + 4);
@@ -204,7 +222,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
 #pragma unroll
-        for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(group_mask, ss, o);
+        for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
         const float inv = rsqrtf(ss * (1.f / D) + p.eps);
         const float *g = is_q ? p.q_gamma : p.k_gamma;
         if (g) {
@@ -219,38 +237,30 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
         }
       }
       if (turns) {
-        const float2 *cs = &s_cs[r][4 * sub];
-        if (p.interleaved) {
+        // pairs (i, 4 + i) of the lane's elements, or (2 i, 2 i + 1)
+        float y[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 t = cs[i];
-            const float u = x[2 * i], w = x[2 * i + 1];
-            x[2 * i] = u * t.x - w * t.y;
-            x[2 * i + 1] = w * t.x + u * t.y;
-          }
-        } else {
+        for (int i = 0; i < 4; ++i) {
+          const float u = p.interleaved ? x[2 * i] : x[i], w = p.interleaved ? x[2 * i + 1] : x[4 + i];
+          y[i] = u * co[i] - w * si[i];
+          y[4 + i] = w * co[i] + u * si[i];
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 t = cs[i];
-            const float u = x[i], w = x[4 + i];
-            x[i] = u * t.x - w * t.y;
-            x[4 + i] = w * t.x + u * t.y;
-          }
+        for (int i = 0; i < 4; ++i) {
+          x[i] = p.interleaved ? y[(i & 1) * 4 + i / 2] : y[i];
+          x[4 + i] = p.interleaved ? y[(i & 1) * 4 + 2 + i / 2] : y[4 + i];
         }
       }
     }
-    const long long row = r0 + r;
     if (is_q || !CACHE) {
-      if (CACHE && s_pos[r] < 0) return;  // a row of no sequence: left as it was
-      uint16_t *dst = is_q ? p.q_out + row * p.q_out_stride + (long long)h * D
-                           : p.k_out + row * p.k_out_stride + (long long)(h - p.n_q) * D;
+      uint16_t *dst = (is_q ? qo_row : ko_row) + (long long)h * D;
       *reinterpret_cast<uint2 *>(dst + e0) = float_to_bf16x4(x);
       *reinterpret_cast<uint2 *>(dst + e1) = float_to_bf16x4(x + 4);
       return;
     }
-    if (!CACHE || s_at[r] < 0) return;
+    if (!CACHE || at < 0) return;
     const int kh = is_v ? h - p.n_q - p.n_kv : h - p.n_q;
-    const long long at = (s_at[r] + (long long)kh * p.page) * D;
+    const long long to = (at + (long long)kh * p.page) * D;
     if (CACHE == 2) {
       const float *scale = is_v ? p.v_scale : p.k_scale;
       if (scale) {
@@ -258,33 +268,28 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = x[i] / s;
       }
-      uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + at;
+      uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + to;
       *reinterpret_cast<uint32_t *>(dst + e0) = float_to_e4m3x4(x);
       *reinterpret_cast<uint32_t *>(dst + e1) = float_to_e4m3x4(x + 4);
     } else {
-      uint16_t *dst = reinterpret_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + at;
+      uint16_t *dst = reinterpret_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + to;
       *reinterpret_cast<uint2 *>(dst + e0) = float_to_bf16x4(x);
       *reinterpret_cast<uint2 *>(dst + e1) = float_to_bf16x4(x + 4);
     }
   };
-  // the next rows' loads go out before the present ones are finished
-  for (int base = 0; base < total; base += NG * PRE) {
+  // the next heads' loads go out before the present ones are finished
+  for (; h < heads; h += PRE * step) {
     uint2 ya[PRE], yb[PRE];
 #pragma unroll
     for (int i = 0; i < PRE; ++i) {
       ya[i] = xa[i];
       yb[i] = xb[i];
+      const int next = h + (PRE + i) * step;
+      if (next < heads) load(next, xa[i], xb[i]);
     }
 #pragma unroll
-    for (int i = 0; i < PRE; ++i) {
-      const int item = base + group + (PRE + i) * NG;
-      if (item < total) load(item, xa[i], xb[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < PRE; ++i) {
-      const int item = base + group + i * NG;
-      if (item < total) finish(item, ya[i], yb[i]);
-    }
+    for (int i = 0; i < PRE; ++i)
+      if (h + i * step < heads) finish(h + i * step, ya[i], yb[i]);
   }
 }
 
