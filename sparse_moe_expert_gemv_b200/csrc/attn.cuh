@@ -99,6 +99,12 @@ MOE_HOST_DEV_INLINE bool keys_seen(const SeqView &s, int window, int n_sink, int
   return (long long)key + n > lo || key < n_sink;
 }
 MOE_HOST_DEV_INLINE int tile_at(const SeqTiles &t, int k) { return k < t.lead ? k : k - t.lead + t.first; }
+// The same list with the leading tiles at its end: a row's first maximum then
+// comes from a full tile of its window, not from a few sinks.
+MOE_HOST_DEV_INLINE int tile_at_lead_last(const SeqTiles &t, int k) {
+  const int rest = t.n - t.lead;
+  return k < rest ? t.first + k : k - rest;
+}
 // Units of a block's run: equal runs over the grid, none shorter than min_units.
 MOE_HOST_DEV_INLINE long long run_length(long long total, long long grid, long long min_units) {
   const unsigned long long x = total + grid - 1;

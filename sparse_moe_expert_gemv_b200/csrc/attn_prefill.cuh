@@ -15,19 +15,32 @@
 //   9, 10  issue the MMAs of tile 0 and 1: S = Q K^T into tensor memory, O +=
 //          P V with P read from tensor memory and V as it lies in the cache
 //          ([key][column]: an MN-major operand).  Issuing is paced by the
-//          tensor cores, so each tile has an issuer of its own: one's waits
-//          are covered by the other's products;
-//   0-3, 4-7  one thread per row of tile 0 and 1, 64 keys a step: reads its
-//          row of S, masks, keeps the running maximum and sum, and writes P
-//          (bf16) over S.
-// S of a tile has two buffers of 64 keys, so the scores of the next step are
-// there while the rows of the present one go through the exponentials.  O
-// stays in tensor memory; it is rescaled only when a row's maximum grew by
-// more than 2^8 over the reference its terms were scaled by (P then holds
-// values up to 2^8, rounded to bf16 like any other; sums are fp32).
+//          tensor cores (64 cycles an MMA), so each tile has an issuer: one's
+//          waits and commits are covered by the other's products.  They take
+//          turns, a step's P V and next S at a time; served together the two
+//          tiles fall into step and wait for the tensor cores and for the
+//          exponentials at the same times (6,200 against 3,800 cycles for 128
+//          keys of both);
+//   0-3, 4-7  one thread per row of tile 0 and 1: reads its row of S, masks,
+//          keeps the running maximum and sum, and writes P (bf16) over S, in
+//          two halves so that the first half's product starts early.
+// While the tensor cores work for one tile, the other's rows go through the
+// exponentials.  O stays in tensor memory; it is rescaled only when a row's
+// maximum grew by more than 2^8 over the reference its terms were scaled by
+// (P then holds values up to 2^8, rounded to bf16 like any other; sums are
+// fp32).
 //
-// Tensor memory: S0, S1 (2 x 64 columns each, P over the first 32 of a
-// buffer), O0, O1.
+// What bounds it: the chain of one tile's step, about 3,800 cycles for 128
+// keys -- S read 390, maximum 330, exponentials 1,530 (a warp per scheduler
+// reaches two thirds of the special function unit's rate), hand-over 230, P V
+// and S 990, commit 360 -- of which the tensor cores work 2,048 for the two
+// tiles.  8192 rows of 16 heads over 16384 keys: 839 us, 983 TFLOP/s.
+// Measured and not kept: two warps per row (927 us), scores double-buffered
+// in steps of 64 keys (876 us: an MMA of 64 columns takes as long as one of
+// 128), exponentials on the FMA units by a polynomial (a quarter of them: 872
+// against 853 us, half: 913).
+//
+// Tensor memory: S0, S1 (128 columns each, P over the first 64), O0, O1.
 #pragma once
 
 #include "attn.cuh"
@@ -37,8 +50,7 @@ namespace moe {
 
 constexpr int kApTile = 128;   // keys of a tile
 constexpr int kApRows = 256;   // rows of a block
-constexpr int kApThreads = 384;  // warp 11 only gives up registers
-constexpr int kApPoly = 1;      // of four pairs of exponentials, those on the FMA units
+constexpr int kApThreads = 384;  // warps 10 and 11 only give up registers
 constexpr float kApSlack = 8.f;  // log2 of the growth that O is not rescaled for
 
 template <int D>
@@ -62,7 +74,7 @@ struct AttnPfParams {
 };
 
 struct AttnPfShared {
-  unsigned long long q_full, kv_full[4], kv_empty[4], s_full[2][2], p_full[2][2], o_done[2], o_full[2], edge, drain[2];
+  unsigned long long q_full, kv_full[4], kv_empty[4], s_full[2], p_full[2][2], o_full[2], turn[2], edge, drain[2];
   long long scan[kApThreads / 32];
   uint32_t tmem;
   int item[2];  // sequence, row block
@@ -130,50 +142,17 @@ MOE_DEV uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x of both on the FMA units: x = n + f with |f| <= 1/2 (n by adding and
-// taking away 1.5 2^23), 2^f by the degree-4 polynomial whose largest relative
-// error on that interval is least (2.6e-6, a least-squares fit reweighted by
-// its own error), n added to the exponent.  x below -126 counts as -126.
-MOE_DEV uint64_t f2_exp2(uint64_t x) {
-  constexpr float kRound = 12582912.f;
-  float a, b;
-  f2_unpack(x, a, b);
-  x = f2_pack(fmaxf(a, -126.f), fmaxf(b, -126.f));
-  const uint64_t t = f2_add(x, f2_pack(kRound, kRound));
-  const uint64_t n = f2_add(t, f2_pack(-kRound, -kRound));
-  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), x);
-  uint64_t y = f2_fma(f2_pack(0.00957006868f, 0.00957006868f), f, f2_pack(0.0559178069f, 0.0559178069f));
-  y = f2_fma(y, f, f2_pack(0.240247443f, 0.240247443f));
-  y = f2_fma(y, f, f2_pack(0.69312185f, 0.69312185f));
-  y = f2_fma(y, f, f2_pack(0.999999285f, 0.999999285f));
-  float t0, t1, y0, y1;
-  f2_unpack(t, t0, t1);
-  f2_unpack(y, y0, y1);
-  y0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23));
-  y1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23));
-  return f2_pack(y0, y1);
-}
-
-// P of 64 columns (two loads' registers) of a row: p = 2^(s scale + neg), the
-// bf16 pairs in w and the sum of both halves added to `sum`.  Of every four
-// pairs POLY go to the FMA units, the others to the special function unit,
-// which alone would take as long as the products.
-template <int POLY>
+// P of 32 columns of a row: p = 2^(s scale + neg), as bf16 pairs in w, their
+// sum added to both halves of `sum`.
 MOE_DEV void row_exp2(const uint32_t (&r)[32], uint64_t scale, uint64_t neg, uint32_t (&w)[16], uint64_t &sum) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), scale, neg);
     float p0, p1;
-    if ((e & 3) >= 4 - POLY) {
-      const uint64_t y = f2_exp2(x);
-      sum = f2_add(sum, y);
-      f2_unpack(y, p0, p1);
-    } else {
-      f2_unpack(x, p0, p1);
-      p0 = ex2(p0);
-      p1 = ex2(p1);
-      sum = f2_add(sum, f2_pack(p0, p1));
-    }
+    f2_unpack(x, p0, p1);
+    p0 = ex2(p0);
+    p1 = ex2(p1);
+    sum = f2_add(sum, f2_pack(p0, p1));
     w[e] = pack_bf16(p0, p1);
   }
 }
@@ -243,12 +222,11 @@ __global__ void __launch_bounds__(kApThreads, 1)
       mbar_init(smem_addr(&sh.kv_empty[i]), 2);
     }
     for (int t = 0; t < 2; ++t) {
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(smem_addr(&sh.s_full[t][h]), 1);
-        mbar_init(smem_addr(&sh.p_full[t][h]), 4);
-      }
-      mbar_init(smem_addr(&sh.o_done[t]), 1);
+      mbar_init(smem_addr(&sh.s_full[t]), 1);
+      mbar_init(smem_addr(&sh.p_full[t][0]), 4);
+      mbar_init(smem_addr(&sh.p_full[t][1]), 4);
       mbar_init(smem_addr(&sh.o_full[t]), 1);
+      mbar_init(smem_addr(&sh.turn[t]), 1);
       mbar_init(smem_addr(&sh.drain[t]), 1);
     }
     mbar_init(smem_addr(&sh.edge), 1);
@@ -300,8 +278,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
     // this lane's box of tile j: whether its page holds a key that is seen,
     // and its row in the cache
     auto box_of = [&](int j, bool &need, int &y) {
-      const int key0 = tile_at(tl, j) * kApTile, pg0 = key0 >> p.page_shift;
-      if (pg0 + ppt > held_at + 32) {
+      const int key0 = tile_at_lead_last(tl, j) * kApTile, pg0 = key0 >> p.page_shift;
+      if (pg0 < held_at || pg0 + ppt > held_at + 32) {
         held = pg0 == held_at + 32 ? ahead : entries(pg0);
         held_at = pg0;
         ahead = entries(pg0 + 32);
@@ -333,7 +311,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
     int issued = 0, edge_uses = 0;
     bool ok = true;
     for (int j = 0; j < tl.n; ++j) {
-      const int key0 = tile_at(tl, j) * kApTile;
+      const int key0 = tile_at_lead_last(tl, j) * kApTile;
       need_k = false;
       if (j + 1 < tl.n) box_of(j + 1, need_k, y_k);
       const int st = j % C::PAIRS, use = j / C::PAIRS;
@@ -360,13 +338,13 @@ __global__ void __launch_bounds__(kApThreads, 1)
       if (edge) {
         ok = mbar_wait_warp(bar, edge_uses & 1, nullptr);
         ++edge_uses;
-        for (int r = 0; r < kApTile; ++r) {
+        for (int r = lane; r < kApTile; r += 32) {
           const int k = key0 + r;
           if (k < s.kv && (k < sink_end || k >= lo)) continue;
-          // a key's line in each half: 8 16-byte pieces
-          if (lane < 8 * C::HALVES)
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (lane >> 3) * C::BOX + r * 128 +
-                                                                       (lane & 7) * 16),
+#pragma unroll
+          for (int i = 0; i < 8 * C::HALVES; ++i)  // a key's line in each half: 8 16-byte pieces
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (i >> 3) * C::BOX + r * 128 +
+                                                                       ((i + r) & 7) * 16),
                          "r"(0)
                          : "memory");
         }
@@ -387,45 +365,47 @@ __global__ void __launch_bounds__(kApThreads, 1)
     few_registers();
     if (lane == 0) {
       const int t = wid - 9;
-      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, 64);
+      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, kApTile);
       constexpr uint32_t IDESC_O = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
       const uint32_t s_at = tmem + t * 128, o_at = tmem + 256 + t * D;
       const uint64_t qd = umma_desc_sw128(q0 + t * C::TILE);
-      auto scores = [&](uint32_t ka, int h) {  // S_h = Q K^T, 64 keys
-        const uint64_t kd = umma_desc_sw128(ka + h * 64 * 128);
+      auto scores = [&](uint32_t ka) {  // S = Q K^T
+        const uint64_t kd = umma_desc_sw128(ka);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          constexpr int box = C::BOX >> 4;
-          umma_f16(s_at + h * 64, qd + (kk >> 2) * box + (kk & 3) * 2, kd + (kk >> 2) * box + (kk & 3) * 2, IDESC_S,
+          constexpr int half = C::BOX >> 4;
+          umma_f16(s_at, qd + (kk >> 2) * half + (kk & 3) * 2, kd + (kk >> 2) * half + (kk & 3) * 2, IDESC_S,
                    kk != 0);
         }
-        umma_commit(smem_addr(&sh.s_full[t][h]));
+        umma_commit(smem_addr(&sh.s_full[t]));
       };
       bool ok = mbar_wait_live(smem_addr(&sh.q_full), 0, &sh.dead);
       if (ok) {
         tc_fence_after();
-        scores(kfirst, 0);
-        scores(kfirst, 1);
+        scores(kfirst);
+        if (t == 1) mbar_arrive(smem_addr(&sh.turn[0]));
       }
       for (int j = 0; j < tl.n && ok; ++j) {
         const int st = j % C::PAIRS;
         const uint32_t va = slot0 + st * 2 * C::TILE;
+        ok = mbar_wait_live(smem_addr(&sh.kv_full[st]), (j / C::PAIRS) & 1, &sh.dead) &&
+             mbar_wait_live(smem_addr(&sh.turn[t]), j & 1, &sh.dead);
         const uint64_t vd = umma_desc_mn_sw128(va, C::BOX);
-        ok = mbar_wait_live(smem_addr(&sh.kv_full[st]), (j / C::PAIRS) & 1, &sh.dead);
         for (int h = 0; h < 2 && ok; ++h) {
           ok = mbar_wait_live(smem_addr(&sh.p_full[t][h]), j & 1, &sh.dead);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // O += P_h V, 64 keys
-            umma_f16_ta(o_at, s_at + h * 64 + kk * 8, vd + (h * 4 + kk) * (2048 >> 4), IDESC_O, (j | h | kk) != 0);
-          umma_commit(smem_addr(&sh.o_done[t]));
-          // in order behind the product that reads P_h, whose columns it overwrites
-          if (j + 1 < tl.n) scores(va + C::TILE, h);
+          for (int kk = 0; kk < 4; ++kk)  // O += P V, 64 keys
+            umma_f16_ta(o_at, s_at + h * 32 + kk * 8, vd + (h * 4 + kk) * (2048 >> 4), IDESC_O, (j | h | kk) != 0);
         }
-        if (ok) umma_commit(smem_addr(&sh.kv_empty[st]));
+        if (!ok) break;
+        // in order behind the product that reads P, whose columns it overwrites
+        if (j + 1 < tl.n) scores(va + C::TILE);
+        else umma_commit(smem_addr(&sh.o_full[t]));
+        mbar_arrive(smem_addr(&sh.turn[t ^ 1]));
+        umma_commit(smem_addr(&sh.kv_empty[st]));
       }
-      umma_commit(smem_addr(&sh.o_full[t]));
       if (!ok) {
         give_up();
         // every issued MMA is complete before tensor memory is released
@@ -447,49 +427,59 @@ __global__ void __launch_bounds__(kApThreads, 1)
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * D;
     float m_ref = -INFINITY, l_run = 0.f;  // m_ref in units of the scores times scale_log2
     bool ok = true;
-    for (int i = 0; i < 2 * tl.n; ++i) {  // 64 keys a step
-      const int h = i & 1, j = i >> 1;
-      ok = mbar_wait_warp(smem_addr(&sh.s_full[t][h]), j & 1, &sh.dead);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t r[2][32];
-      tmem_ld32_issue(s_at + h * 64, r[0]);
-      tmem_ld32_issue(s_at + h * 64 + 32, r[1]);
-      const int key0 = tile_at(tl, j) * kApTile + h * 64;
+    for (int j = 0; j < tl.n; ++j) {
+      const int key0 = tile_at_lead_last(tl, j) * kApTile;
       // visible columns: c <= hi by position; with a window c >= lo or c < sk
       const int hi = pos - key0;
       const int lo = p.window > 0 ? hi - p.window + 1 : 0;  // |hi| < 2^31 - window: no overflow
       const int sk = p.n_sink - key0;
-      const bool masked = __any_sync(0xffffffffu, !(hi >= 63 && (lo <= 0 || sk >= 64)));
+      const bool masked = __any_sync(0xffffffffu, !(hi >= kApTile - 1 && (lo <= 0 || sk >= kApTile)));
+      ok = mbar_wait_live(smem_addr(&sh.s_full[t]), j & 1, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[4][32];
+      tmem_ld32_issue(s_at, r[0]);
+      tmem_ld32_issue(s_at + 32, r[1]);
       tmem_ld32_wait(r[0]);
       tmem_ld32_wait(r[1]);
-      if (masked) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c > hi || (c < lo && c >= sk)) r[c >> 5][c & 31] = 0xff800000u;  // -inf
-      }
+      tmem_ld32_issue(s_at + 64, r[2]);
+      tmem_ld32_issue(s_at + 96, r[3]);
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };  // bits [0, n)
+      auto look = [&](int c) {  // masks 32 columns and takes their maximum
+        if (masked) {
+          // a bit per visible column of these 32
+          const uint32_t vis = below(hi + 1 - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
 #pragma unroll
-      for (int c = 0; c < 64; c += 8)
+          for (int e = 0; e < 32; ++e)
+            if (!(vis >> e & 1u)) r[c][e] = 0xff800000u;  // -inf
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(r[c >> 5][(c & 31) + 2 * e]),
-                                     __uint_as_float(r[c >> 5][(c & 31) + 2 * e + 1])));
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            m4[k] = fmaxf(m4[k], fmaxf(__uint_as_float(r[c][e + 2 * k]), __uint_as_float(r[c][e + 2 * k + 1])));
+      };
+      look(0);
+      look(1);
+      tmem_ld32_wait(r[2]);
+      tmem_ld32_wait(r[3]);
+      look(2);
+      look(3);
       const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-      // the reference follows the maximum when it fell 2^kApSlack behind
+      // the reference follows the maximum when it fell 2^kApSlack behind (the
+      // commit that brought S also says that O holds every earlier product)
+      const bool first = m_ref == -INFINITY;
+      const bool grow = mx > m_ref + kApSlack;
       float corr = 1.f;
-      if (m_ref == -INFINITY) {
+      if (first) {
         m_ref = mx;
-      } else if (mx > m_ref + kApSlack) {
+      } else if (grow) {
         corr = ex2(m_ref - mx);
         m_ref = mx;
       }
-      if (__any_sync(0xffffffffu, corr != 1.f)) {  // (never in the first step)
-        // O holds every earlier product once the last one is through, and the
-        // next one waits for the P of this step
-        ok = mbar_wait_warp(smem_addr(&sh.o_done[t]), (i - 1) & 1, &sh.dead);
-        if (!ok) break;
-        tc_fence_after();
+      if (__any_sync(0xffffffffu, corr != 1.f)) {
         l_run *= corr;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -505,18 +495,17 @@ __global__ void __launch_bounds__(kApThreads, 1)
       const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), neg2 = f2_pack(neg, neg);
       uint64_t sum = 0;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t w[16];
-        // (masked columns need a true zero, which only the special function
-        // unit's path gives)
-        if (masked) row_exp2<0>(r[c], scale2, neg2, w, sum);
-        else row_exp2<kApPoly>(r[c], scale2, neg2, w, sum);
-        tmem_st16(s_at + h * 64 + c * 16, w);
+        row_exp2(r[c], scale2, neg2, w, sum);
+        tmem_st16(s_at + c * 16, w);
+        if (c & 1) {  // half of the keys: their product can start
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[t][c >> 1]));
+        }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[t][h]));
       float sum0, sum1;
       f2_unpack(sum, sum0, sum1);
       l_run += sum0 + sum1;

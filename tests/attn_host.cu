@@ -38,6 +38,9 @@ static void tiles() {
             before = tile;
             got.insert(tile);
           }
+          std::set<int> again;
+          for (int k = 0; k < t.n; ++k) again.insert(tile_at_lead_last(t, k));
+          CHECK(again == got);
           std::set<int> want;
           for (int j = 0; j < kv; ++j) {
             bool seen = false;
