@@ -221,7 +221,11 @@ moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_st
   if (!rows_ok(q, q_stride, width, 16) || !rows_ok(out, out_stride, width, 16))
     return fail(c, MOE_ERR_INVALID_ARG, "%s: q and out rows are 16-byte aligned, at least n_q * head_dim apart", who);
   c->last_stream = (cudaStream_t)stream;
-  if (chunk && a.cache == MOE_KV_BF16 && (long long)max_T * (a.n_q / a.n_kv) > kAtMaxRows)
+  // Few rows cannot give the chunk kernel's blocks of 256 rows to enough SMs,
+  // while the window kernel splits their keys over all of them: 128 rows of 16
+  // heads of 128 over 16384 keys take 99 us there, against 244 us; 512 rows
+  // 320 us, against 245 us.
+  if (chunk && a.cache == MOE_KV_BF16 && (long long)b->n_rows * a.n_q > 10 * kApRows)
     return attend_chunk(c, b, q, q_stride, scale, window, n_sink, out, out_stride, (cudaStream_t)stream, who);
   CUtensorMap km, vm;
   const int box = a.page < kAtTile ? a.page : kAtTile;
