@@ -82,7 +82,8 @@ moe_status kv_rows(moe_ctx *c, cudaStream_t s, KvRowsParams &p, const moe_qk_nor
 
 // 2-D map of a paged cache seen as [n_pages * n_kv * page][D]: boxes of one
 // page's keys (at most a tile's) x one swizzle row.
-bool encode_cache_map(CUtensorMap *map, const moe_ctx::Attn &a, const void *base, int n_pages, int box_keys) {
+bool encode_cache_map(CUtensorMap *map, const moe_ctx::Attn &a, const void *base, int n_pages, int box_keys,
+                      bool swizzle = true) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
   const bool fp8 = a.cache == MOE_KV_E4M3;
@@ -93,7 +94,8 @@ bool encode_cache_map(CUtensorMap *map, const moe_ctx::Attn &a, const void *base
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -114,6 +116,12 @@ cudaError_t setup_attn_all(int *blocks) {
   if (e == cudaSuccess) e = setup_attn<D, FP8, 2>(blocks);
   if (e == cudaSuccess) e = setup_attn<D, FP8, 4>(blocks);
   return e;
+}
+
+template <int D, bool FP8>
+cudaError_t setup_attn_prefill() {
+  return cudaFuncSetAttribute(attn_prefill_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              AttnPfCfg<D, FP8>::SMEM);
 }
 
 template <int D, bool FP8, int MT>
@@ -153,23 +161,23 @@ bool encode_q_map(CUtensorMap *map, const moe_ctx::Attn &a, const void *q, int n
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool FP8>
 cudaError_t launch_attn_prefill(cudaStream_t s, int grid, const CUtensorMap &qm, const CUtensorMap &km,
                                 const CUtensorMap &vm, const AttnPfParams &p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kApThreads);
-  cfg.dynamicSmemBytes = AttnPfCfg<D>::SMEM;
+  cfg.blockDim = dim3(AttnPfCfg<D, FP8>::THREADS);
+  cfg.dynamicSmemBytes = AttnPfCfg<D, FP8>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, qm, km, vm, p);
+  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, FP8>, qm, km, vm, p);
 }
 
-// The tensor-core kernel over a bf16 cache.
+// The tensor-core kernel.
 moe_status attend_chunk(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_stride, float scale, int window,
                         int n_sink, void *out, int64_t out_stride, cudaStream_t s, const char *who) {
   const moe_ctx::Attn &a = c->attn;
@@ -194,16 +202,25 @@ moe_status attend_chunk(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_
   p.page = a.page;
   while ((1 << p.page_shift) < a.page) ++p.page_shift;
   p.status = a.status;
+  p.k_scale = b->k_scale;
+  p.v_scale = b->v_scale;
+  const bool fp8 = a.cache == MOE_KV_E4M3;  // its tiles are converted on the way: no swizzle
   CUtensorMap qm, km, vm;
   const int box = a.page < kApTile ? a.page : kApTile;
-  if (!encode_q_map(&qm, a, q, b->n_rows, q_stride, p.pack) || !encode_cache_map(&km, a, b->k, b->n_pages, box) ||
-      !encode_cache_map(&vm, a, b->v, b->n_pages, box))
+  if (!encode_q_map(&qm, a, q, b->n_rows, q_stride, p.pack) || !encode_cache_map(&km, a, b->k, b->n_pages, box, !fp8) ||
+      !encode_cache_map(&vm, a, b->v, b->n_pages, box, !fp8))
     return fail(c, MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
   // the row blocks of all sequences are at most this many (the rest leave at once)
   const long long blocks = (long long)b->n_rows / (kApRows / p.pack) + b->n_seqs, grid = blocks * (a.n_q / p.pack);
   if (grid > 0x7fffffffLL) return fail(c, MOE_ERR_NOT_SUPPORTED, "%s: %lld blocks", who, grid);
-  CUDA_TRY(c, a.dim == 128 ? launch_attn_prefill<128>(s, (int)grid, qm, km, vm, p)
-                           : launch_attn_prefill<64>(s, (int)grid, qm, km, vm, p));
+  cudaError_t e;
+  if (a.dim == 128)
+    e = fp8 ? launch_attn_prefill<128, true>(s, (int)grid, qm, km, vm, p)
+            : launch_attn_prefill<128, false>(s, (int)grid, qm, km, vm, p);
+  else
+    e = fp8 ? launch_attn_prefill<64, true>(s, (int)grid, qm, km, vm, p)
+            : launch_attn_prefill<64, false>(s, (int)grid, qm, km, vm, p);
+  CUDA_TRY(c, e);
   return MOE_OK;
 }
 
@@ -225,7 +242,7 @@ moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_st
   // while the window kernel splits their keys over all of them: 128 rows of 16
   // heads of 128 over 16384 keys take 99 us there, against 244 us; 512 rows
   // 320 us, against 245 us.
-  if (chunk && a.cache == MOE_KV_BF16 && (long long)b->n_rows * a.n_q > 10 * kApRows)
+  if (chunk && (long long)b->n_rows * a.n_q > 10 * kApRows)
     return attend_chunk(c, b, q, q_stride, scale, window, n_sink, out, out_stride, (cudaStream_t)stream, who);
   CUtensorMap km, vm;
   const int box = a.page < kAtTile ? a.page : kAtTile;
@@ -293,11 +310,9 @@ moe_status moe_attn_configure(moe_ctx *c, int n_q, int n_kv, int head_dim, int p
   int blocks = kAtGridPerSm;
   cudaError_t e = head_dim == 128 ? (fp8 ? setup_attn_all<128, true>(&blocks) : setup_attn_all<128, false>(&blocks))
                                   : (fp8 ? setup_attn_all<64, true>(&blocks) : setup_attn_all<64, false>(&blocks));
-  if (e == cudaSuccess && !fp8)
-    e = head_dim == 128 ? cudaFuncSetAttribute(attn_prefill_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               AttnPfCfg<128>::SMEM)
-                        : cudaFuncSetAttribute(attn_prefill_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               AttnPfCfg<64>::SMEM);
+  if (e == cudaSuccess)
+    e = head_dim == 128 ? (fp8 ? setup_attn_prefill<128, true>() : setup_attn_prefill<128, false>())
+                        : (fp8 ? setup_attn_prefill<64, true>() : setup_attn_prefill<64, false>());
   CUDA_TRY(c, e);
   if (blocks < 1) return fail(c, MOE_ERR_CUDA, "moe_attn_configure: the attention kernel does not fit this device");
   a.grid = c->n_sm * blocks;

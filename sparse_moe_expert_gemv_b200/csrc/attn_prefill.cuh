@@ -50,22 +50,30 @@ namespace moe {
 
 constexpr int kApTile = 128;   // keys of a tile
 constexpr int kApRows = 256;   // rows of a block
-constexpr int kApThreads = 384;  // warps 10 and 11 only give up registers
 constexpr float kApSlack = 8.f;  // log2 of the growth that O is not rescaled for
 
-template <int D>
+template <int D, bool FP8>
 struct AttnPfCfg {
   static constexpr int HALVES = D / 64;                // 128-byte column boxes
   static constexpr int BOX = kApTile * 128;            // 128 rows x 64 columns
-  static constexpr int TILE = HALVES * BOX;            // a query, key or value tile
+  static constexpr int TILE = HALVES * BOX;            // a query, key or value tile (bf16)
   static constexpr int PAIRS = D == 128 ? 2 : 4;       // ring of (value tile, next key tile)
-  static constexpr int SMEM = 1024 + 2 * TILE + (1 + 2 * PAIRS) * TILE;
+  static constexpr int RAW = kApTile * D;              // an e4m3 tile as it lies in the cache
+  // rows, producer, two issuers, a spare; e4m3: four converting warps
+  static constexpr int THREADS = FP8 ? 512 : 384;
+  // registers of the rows' threads and of the others: together those of the launch
+  static constexpr int ROW_REGS = FP8 ? 208 : 216, OTHER_REGS = FP8 ? 48 : 72;
+  static_assert(256 * ROW_REGS + (THREADS - 256) * OTHER_REGS == THREADS * (65536 / THREADS / 8 * 8), "");
+  // queries, the ring, and the first keys' tile or (e4m3, whose first keys lie
+  // in the last pair's place) two raw tiles
+  static constexpr int SMEM = 1024 + 2 * TILE + 2 * PAIRS * TILE + (FP8 ? 2 * RAW : TILE);
 };
 
 struct AttnPfParams {
   uint16_t *out;
   long long out_stride;
   const int *page_table, *row_off, *kv_len;
+  const float *k_scale, *v_scale;  // e4m3: [n_kv] or null
   float scale_log2;
   int window, n_sink;
   int n_rows, n_q, n_kv, group, pack, pack_shift;
@@ -75,7 +83,8 @@ struct AttnPfParams {
 
 struct AttnPfShared {
   unsigned long long q_full, kv_full[4], kv_empty[4], s_full[2], p_full[2][2], o_full[2], turn[2], edge, drain[2];
-  long long scan[kApThreads / 32];
+  unsigned long long k0_full, raw_full[2], raw_empty[2];  // e4m3
+  long long scan[16];
   uint32_t tmem;
   int item[2];  // sequence, row block
   int dead;
@@ -162,15 +171,17 @@ MOE_DEV void mbar_expect_only(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kApThreads, 1)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const AttnPfParams p) {
-  using C = AttnPfCfg<D>;
+  using C = AttnPfCfg<D, FP8>;
+  constexpr int kApThreads = C::THREADS;
   extern __shared__ __align__(1024) unsigned char ap_smem[];
   AttnPfShared &sh = *reinterpret_cast<AttnPfShared *>(ap_smem);
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
-  const uint32_t q0 = smem_addr(ap_smem) + 1024, kfirst = q0 + 2 * C::TILE, slot0 = kfirst + C::TILE;
+  const uint32_t q0 = smem_addr(ap_smem) + 1024, slot0 = q0 + 2 * C::TILE, raw0 = slot0 + 2 * C::PAIRS * C::TILE;
+  const uint32_t kfirst = FP8 ? slot0 + (2 * C::PAIRS - 1) * C::TILE : raw0;
   pdl_wait();
 
   // ---- this block's item: head group fastest (blocks that share keys run
@@ -218,7 +229,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
   if (tid == 0) {
     mbar_init(smem_addr(&sh.q_full), 1);
     for (int i = 0; i < C::PAIRS; ++i) {
-      mbar_init(smem_addr(&sh.kv_full[i]), 1);
+      mbar_init(smem_addr(&sh.kv_full[i]), FP8 ? 8 : 1);  // e4m3: four warps, values and keys
       mbar_init(smem_addr(&sh.kv_empty[i]), 2);
     }
     for (int t = 0; t < 2; ++t) {
@@ -230,6 +241,11 @@ __global__ void __launch_bounds__(kApThreads, 1)
       mbar_init(smem_addr(&sh.drain[t]), 1);
     }
     mbar_init(smem_addr(&sh.edge), 1);
+    mbar_init(smem_addr(&sh.k0_full), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.raw_full[i]), 1);
+      mbar_init(smem_addr(&sh.raw_empty[i]), 4);
+    }
     sh.dead = 0;
     fence_mbar_init();
   }
@@ -257,18 +273,20 @@ __global__ void __launch_bounds__(kApThreads, 1)
     atomicOr(p.status, kErrTimeout);
   };
 
-  // 168 registers a thread at launch (384 threads): the rows' warps take 216
-  // of the last four's share: 256 * 216 + 128 * 72 = 384 * 168
-  auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); };
+  auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS)); };
+  // keys that some row of the sequence sees: [0, sink_end) and [seen_lo, kv).
+  // Values outside may hold anything: such rows of a value tile become zeros
+  // before the tensor cores read them.
+  const long long seen_lo = p.window > 0 ? (long long)pos0 - p.window + 1 : 0;
+  const int sink_end = seen_lo > 0 ? (int)min((long long)p.n_sink, seen_lo) : 0;
+  auto seen_by_some = [&](int k) { return k < s.kv && (k < sink_end || k >= seen_lo); };
   if (wid == 8) {
     // ---------------------------------------------------------- producer
     few_registers();
     const int pr = min(p.page, kApTile);
     const int ppt = kApTile / pr;  // boxes along a tile's keys, at most 8
-    // keys that some row of the sequence sees: [0, sink_end) and [lo, kv)
-    const long long lo = p.window > 0 ? (long long)pos0 - p.window + 1 : 0;
-    const int sink_end = lo > 0 ? (int)min((long long)p.n_sink, lo) : 0;
-    const int my_page = lane / C::HALVES, my_half = lane % C::HALVES;
+    constexpr int COLS = FP8 ? 1 : C::HALVES;  // column boxes of a page
+    const int my_page = lane / COLS, my_half = lane % COLS;
     // 32 entries of the page table, one per lane, and the 32 behind them
     // already on their way: a look-up is never waited for between tiles
     const int n_pg = (s.kv + p.page - 1) >> p.page_shift;  // pages that hold keys
@@ -286,38 +304,66 @@ __global__ void __launch_bounds__(kApThreads, 1)
       }
       const int first_key = key0 + my_page * pr;
       int page = __shfl_sync(0xffffffffu, held, min(pg0 - held_at + my_page, 31));
-      need = lane < ppt * C::HALVES && keys_seen(s, p.window, p.n_sink, first_key, pr);
+      need = lane < ppt * COLS && keys_seen(s, p.window, p.n_sink, first_key, pr);
       if (need && (unsigned)page >= (unsigned)p.n_pages) {
         atomicOr(p.status, kErrBadPage);
         page = 0;  // an in-bounds page; the call's result is reported as bad
       }
       y = (page * p.n_kv + kv_h) * p.page + (first_key & (p.page - 1));
     };
-    const uint32_t box_at = my_half * C::BOX + my_page * pr * 128;
-    auto bytes_of = [&](bool need) { return (uint32_t)__popc(__ballot_sync(0xffffffffu, need)) * pr * 128; };
-    bool need, need_k;
-    int y, y_k;
-    box_of(0, need, y);
-    const uint32_t bytes0 = bytes_of(need), q_bar = smem_addr(&sh.q_full);
-    if (lane == 0) {  // the queries and the first keys
-      mbar_expect_tx(q_bar, 2 * C::TILE + bytes0);
+    constexpr int LINE = FP8 ? D : 128;  // bytes of a box row
+    const uint32_t box_at = my_half * C::BOX + my_page * pr * LINE;
+    auto bytes_of = [&](bool need) { return (uint32_t)__popc(__ballot_sync(0xffffffffu, need)) * pr * LINE; };
+    auto load_queries = [&](uint32_t bar) {
       for (int t = 0; t < 2; ++t)
         for (int h = 0; h < C::HALVES; ++h)
           tma_load_3d(q0 + t * C::TILE + h * C::BOX, &qmap, h * 64, hg << p.pack_shift,
-                      s.row0 + t_lo + t * (tokens / 2), q_bar);
+                      s.row0 + t_lo + t * (tokens / 2), bar);
+    };
+    const uint32_t q_bar = smem_addr(&sh.q_full);
+    bool ok = true;
+    if constexpr (FP8) {
+      // the raw tiles in the order they are used: K0, V0, K1, V1, ...
+      if (lane == 0) {
+        mbar_expect_tx(q_bar, 2 * C::TILE);
+        load_queries(q_bar);
+      }
+      bool need = false;
+      int y = 0, issued = 0;
+      for (int i = 0; i < 2 * tl.n; ++i) {
+        if (!(i & 1)) box_of(i >> 1, need, y);
+        const int st = i & 1, use = i >> 1;
+        const uint32_t bytes = bytes_of(need), bar = smem_addr(&sh.raw_full[st]);
+        if (use > 0) ok = mbar_wait_warp(smem_addr(&sh.raw_empty[st]), (use - 1) & 1, &sh.dead);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(bar, bytes);
+        __syncwarp();
+        if (need) tma_load_2d(raw0 + st * C::RAW + box_at, i & 1 ? &vmap : &kmap, 0, y, bar);
+        ++issued;
+      }
+      if (!ok && lane == 0) give_up();
+      // no tile may land after the block has gone
+      (void)mbar_wait_bounded(q_bar, 0);
+      for (int i = max(0, issued - 2); i < issued; ++i)
+        (void)mbar_wait_bounded(smem_addr(&sh.raw_full[i & 1]), (i >> 1) & 1);
+    } else {
+    bool need, need_k;
+    int y, y_k;
+    box_of(0, need, y);
+    const uint32_t bytes0 = bytes_of(need);
+    if (lane == 0) {  // the queries and the first keys
+      mbar_expect_tx(q_bar, 2 * C::TILE + bytes0);
+      load_queries(q_bar);
     }
     __syncwarp();
     if (need) tma_load_2d(kfirst + box_at, &kmap, my_half * 64, y, q_bar);
     int issued = 0, edge_uses = 0;
-    bool ok = true;
     for (int j = 0; j < tl.n; ++j) {
       const int key0 = tile_at_lead_last(tl, j) * kApTile;
       need_k = false;
       if (j + 1 < tl.n) box_of(j + 1, need_k, y_k);
       const int st = j % C::PAIRS, use = j / C::PAIRS;
-      // values no row of the sequence sees may hold anything: such rows of
-      // the tile become zeros before the tensor cores read them
-      const bool edge = key0 + kApTile > s.kv || (key0 < lo && key0 + kApTile > sink_end);
+      const bool edge = key0 + kApTile > s.kv || (key0 < seen_lo && key0 + kApTile > sink_end);
       const uint32_t bytes_v = bytes_of(need), bytes_k = bytes_of(need_k);
       if (use > 0) ok = mbar_wait_warp(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
       if (!ok) break;
@@ -339,8 +385,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         ok = mbar_wait_warp(bar, edge_uses & 1, nullptr);
         ++edge_uses;
         for (int r = lane; r < kApTile; r += 32) {
-          const int k = key0 + r;
-          if (k < s.kv && (k < sink_end || k >= lo)) continue;
+          if (seen_by_some(key0 + r)) continue;
 #pragma unroll
           for (int i = 0; i < 8 * C::HALVES; ++i)  // a key's line in each half: 8 16-byte pieces
             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst + (i >> 3) * C::BOX + r * 128 +
@@ -360,6 +405,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
     (void)mbar_wait_bounded(q_bar, 0);
     for (int j = max(0, issued - C::PAIRS); j < issued; ++j)
       (void)mbar_wait_bounded(smem_addr(&sh.kv_full[j % C::PAIRS]), (j / C::PAIRS) & 1);
+    }
   } else if (wid == 9 || wid == 10) {
     // ------------------------------------- MMA issuers, one per row tile
     few_registers();
@@ -380,9 +426,11 @@ __global__ void __launch_bounds__(kApThreads, 1)
         umma_commit(smem_addr(&sh.s_full[t]));
       };
       bool ok = mbar_wait_live(smem_addr(&sh.q_full), 0, &sh.dead);
+      if (FP8) ok = ok && mbar_wait_live(smem_addr(&sh.k0_full), 0, &sh.dead);
       if (ok) {
         tc_fence_after();
         scores(kfirst);
+        if (FP8) umma_commit(smem_addr(&sh.kv_empty[C::PAIRS - 1]));  // the first keys' place
         if (t == 1) mbar_arrive(smem_addr(&sh.turn[0]));
       }
       for (int j = 0; j < tl.n && ok; ++j) {
@@ -415,9 +463,62 @@ __global__ void __launch_bounds__(kApThreads, 1)
     }
   } else if (wid == 11) {
     few_registers();
+  } else if (FP8 && wid >= 12) {
+    // ------------------- converting warps: e4m3 tiles to bf16, which holds
+    // every e4m3 value; the scales go to the scores and the output
+    few_registers();
+    const int c16 = tid % (D / 16);  // this lane's 16 columns
+    bool ok = true;
+    for (int i = 0; i <= 2 * tl.n && ok; ++i) {
+      // tile i: key tile i / 2, or value tile i / 2; key tile n does not exist
+      const int j = i >> 1, st = i & 1;
+      const bool is_v = i & 1, there = i < 2 * tl.n;
+      const int pair = i == 0 ? C::PAIRS - 1 : (is_v ? j : j - 1) % C::PAIRS;
+      const uint32_t dst = slot0 + (2 * pair + (is_v ? 0 : 1)) * C::TILE;
+      if (is_v) {  // the pair's place is free (the last pair's held the first keys)
+        const int free = j / C::PAIRS - (pair == C::PAIRS - 1 ? 0 : 1);
+        if (free >= 0) ok = mbar_wait_warp(smem_addr(&sh.kv_empty[pair]), free & 1, &sh.dead);
+      }
+      if (there && ok) {
+        ok = mbar_wait_warp(smem_addr(&sh.raw_full[st]), j & 1, &sh.dead);
+        if (ok) {
+          const int key0 = tile_at_lead_last(tl, j) * kApTile;
+          const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < seen_lo && key0 + kApTile > sink_end));
+#pragma unroll 2
+          for (int r = (tid & 127) / (D / 16); r < kApTile; r += 128 / (D / 16)) {
+            uint4 v = lds_u4(raw0 + st * C::RAW + r * D + c16 * 16);
+            if (edge && !seen_by_some(key0 + r)) v = make_uint4(0, 0, 0, 0);
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            uint32_t out[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t h = e4m3x2_to_f16x2(in[e >> 1] >> (16 * (e & 1)));
+              out[e] = pack_bf16(half_lo(h), half_hi(h));
+            }
+            // 16 columns: two 16-byte pieces of the row's line, swizzled by the row
+            const uint32_t line = dst + (c16 >> 2) * C::BOX + r * 128;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                               line + (((2 * (c16 & 3) + e) ^ (r & 7)) << 4)),
+                           "r"(out[4 * e]), "r"(out[4 * e + 1]), "r"(out[4 * e + 2]), "r"(out[4 * e + 3])
+                           : "memory");
+          }
+        }
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();  // the tensor cores read the tile through the async proxy
+      __syncwarp();
+      if (lane == 0) {
+        if (there) mbar_arrive(smem_addr(&sh.raw_empty[st]));
+        mbar_arrive(i == 0 ? smem_addr(&sh.k0_full) : smem_addr(&sh.kv_full[pair]));
+      }
+    }
+    if (!ok && lane == 0) give_up();
   } else {
     // -------------------------------------------------- one thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::ROW_REGS));
+    const float scale_log2 = p.scale_log2 * (FP8 && p.k_scale ? __ldg(p.k_scale + kv_h) : 1.f);
     const int t = wid >> 2, row = (wid & 3) * 32 + lane;
     const int tok = t_lo + t * (tokens / 2) + (row >> p.pack_shift);
     const int head = (hg << p.pack_shift) + (row & (p.pack - 1));
@@ -431,8 +532,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
       const int key0 = tile_at_lead_last(tl, j) * kApTile;
       // visible columns: c <= hi by position; with a window c >= lo or c < sk
       const int hi = pos - key0;
-      const int lo = p.window > 0 ? hi - p.window + 1 : 0;  // |hi| < 2^31 - window: no overflow
-      const int sk = p.n_sink - key0;
+      const int lo = p.window > 0 ? (int)max(0LL, (long long)hi - p.window + 1) : 0;
+      const int sk = max(0, p.n_sink - key0);
       const bool masked = __any_sync(0xffffffffu, !(hi >= kApTile - 1 && (lo <= 0 || sk >= kApTile)));
       ok = mbar_wait_live(smem_addr(&sh.s_full[t]), j & 1, &sh.dead);
       ok = __all_sync(0xffffffffu, ok);
@@ -467,7 +568,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
       tmem_ld32_wait(r[3]);
       look(2);
       look(3);
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale_log2;
       // the reference follows the maximum when it fell 2^kApSlack behind (the
       // commit that brought S also says that O holds every earlier product)
       const bool first = m_ref == -INFINITY;
@@ -492,7 +593,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         }
       }
       const float neg = m_ref == -INFINITY ? 0.f : -m_ref;  // nothing seen yet: 2^-inf = 0
-      const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), neg2 = f2_pack(neg, neg);
+      const uint64_t scale2 = f2_pack(scale_log2, scale_log2), neg2 = f2_pack(neg, neg);
       uint64_t sum = 0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -513,7 +614,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
     if (ok) ok = mbar_wait_warp(smem_addr(&sh.o_full[t]), 0, &sh.dead);
     if (ok) {
       tc_fence_after();
-      const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+      const float vs = FP8 && p.v_scale ? __ldg(p.v_scale + kv_h) : 1.f;
+      const float inv = l_run > 0.f || l_run != l_run ? vs / l_run : 0.f;
       uint16_t *dst = p.out + (long long)(s.row0 + tok) * p.out_stride + (long long)head * D;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {

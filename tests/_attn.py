@@ -64,7 +64,7 @@ class Cache:
                          k_scale=self.k_scale, v_scale=self.v_scale)
 
 
-def attention64(q, cache, rows, scale, window, sinks):
+def attention64(q, cache, rows, scale, window, sinks, chunk=False):
     """(o, tol) in fp64 for q [n, n_q, dim].
 
     tol bounds the kernels' rounding, derived term by term.  With
@@ -73,9 +73,10 @@ def attention64(q, cache, rows, scale, window, sinks):
                 so each probability is off by a factor within 1 +- 2 ds (a
                 probability and the sum it is divided by), and by 2^-20 for
                 ex2 and the maximum's multiple;
-      p         rounded to bf16, 2^-8 of itself; with an e4m3 cache to fp16,
-                2^-11 of itself and 2^-25 where it is subnormal (the sum is at
-                least 1): n 2^-25 max |v|;
+      p         rounded to bf16, 2^-8 of itself (chunks, and windows over a
+                bf16 cache); in windows over an e4m3 cache to fp16, 2^-11 of
+                itself and 2^-25 where it is subnormal (the sum is at least 1):
+                n 2^-25 max |v|;
       q         (e4m3 caches) fp16 after division by a power of two: exact but
                 for elements below 2^-14 of the row's largest, 2^-25 of it:
                 |ds| <= scale 2^-24 max|q| sum |k|;
@@ -107,7 +108,7 @@ def attention64(q, cache, rows, scale, window, sinks):
                 ds = ds + scale * 2.0 ** -24 * qh.abs().amax(-1, keepdim=True) * kh.abs().sum(-1).max()
             a = p @ vh.abs()
             oh = p @ vh
-            t = (2.0 ** -11 if cache.e4m3 else 2.0 ** -8) * a + (2 * ds + 2.0 ** -20) * a + 2.0 ** -8 * oh.abs()
+            t = (2.0 ** -11 if cache.e4m3 and not chunk else 2.0 ** -8) * a + (2 * ds + 2.0 ** -20) * a + 2.0 ** -8 * oh.abs()
             if cache.e4m3:
                 t = t + n * 2.0 ** -25 * vh.abs().max()
             o[at:at + r, h], tol[at:at + r, h] = oh, t * (1 + 2.0 ** -6)

@@ -211,7 +211,7 @@ def run_attention(B, make_ctx, fn, e4m3, rows, kv, page, n_q, n_kv, dim, window,
     batch = cache.batch(B, rows, extra)
     fn(ctx, batch, q, max(rows), scale, window, sinks, out)
     B.moe_sync(ctx, 60000)
-    want, tol = A.attention64(q[:n], cache, rows, scale, window, sinks)
+    want, tol = A.attention64(q[:n], cache, rows, scale, window, sinks, chunk=fn is B.moe_attn_prefill)
     close(out[:n], want, tol)
     assert (out[n:] == 3).all()
     # the same call again gives the same bits, and so does out = q
@@ -395,6 +395,10 @@ CHUNKS = [
     ([40], [10], 16, 16, 16, 64, 0, 0),             # replaced below by kv = rows
     ([2100], [2100], 64, 16, 4, 128, 1024, 70),
     ([70] * 20, [70 + 31 * i for i in range(20)], 32, 8, 2, 128, 0, 0),
+    ([300], [900], 16, 16, 16, 128, 0, 0),          # one head per tile
+    ([2000], [2500], 128, 3, 1, 64, 90, 5),
+    ([520, 0, 1], [520, 0, 700], 16, 8, 2, 64, 0, 0),
+    ([40] * 50, [40 + i for i in range(50)], 16, 16, 2, 64, 30, 1),  # more than 32 sequences
 ]
 CHUNKS = [(r, [max(a, b) for a, b in zip(r, k)], *rest) for r, k, *rest in CHUNKS]
 
@@ -421,6 +425,6 @@ def test_scores_that_keep_growing(B, make_ctx, e4m3, rows):
         fn = B.moe_attn_forward if rows <= 32 else B.moe_attn_prefill
         fn(ctx, cache.batch(B, [rows]), q, rows, 1 / math.sqrt(128), 0, 0, out)
         cache.kv = [1500]
-        want, tol = A.attention64(q, cache, [rows], 1 / math.sqrt(128), 0, 0)
+        want, tol = A.attention64(q, cache, [rows], 1 / math.sqrt(128), 0, 0, chunk=rows > 32)
         close(out, want, tol)
     B.moe_sync(ctx, 60000)
