@@ -422,10 +422,12 @@ MOE_API moe_status moe_kv_append(moe_ctx *ctx, const moe_kv_batch *batch, const 
  * [n_rows, n_q, head_dim], 16-byte aligned, row strides in elements,
  * multiples of 8; out may be q itself.  fp32 accumulation and softmax
  * statistics; probabilities enter the product with the values in bf16 (fp16
- * with an e4m3 cache).  Cache rows that no row of their sequence sees may
+ * where an e4m3 cache is read for at most 64 rows, max_T * n_q / n_kv, of a
+ * KV head).  Cache rows that no row of their sequence sees may
  * hold anything; a NaN or infinite value that some row sees may reach the
  * call's other rows of that sequence.  The cache's length is split over the
- * GPU and joined within the launch; results do not depend on timing.
+ * GPU and joined within the launch; results do not depend on timing.  A
+ * sequence with more rows than max_T is served correctly, only slower.
  * Errors: INVALID_ARG, STATE, NOT_SUPPORTED (2^31 or more cache rows). */
 MOE_API moe_status moe_attn_forward(moe_ctx *ctx, const moe_kv_batch *batch, const void *q,
                                     int64_t q_stride, int max_T, float scale, int window,

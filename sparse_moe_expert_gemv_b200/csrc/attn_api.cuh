@@ -213,19 +213,26 @@ moe_status attend_chunk(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_
   // the row blocks of all sequences are at most this many (the rest leave at once)
   const long long blocks = (long long)b->n_rows / (kApRows / p.pack) + b->n_seqs, grid = blocks * (a.n_q / p.pack);
   if (grid > 0x7fffffffLL) return fail(c, MOE_ERR_NOT_SUPPORTED, "%s: %lld blocks", who, grid);
+  // few blocks: the spare SMs take parts of their keys (the workspace has room
+  // for n_sm parts of 256 rows)
+  p.bases = (int)grid;
+  const long long room = (long long)a.grid * 2 * kAtMaxRows / kApRows;
+  p.max_split = grid <= 0x7fffffff / 2 ? (int)std::max(1LL, std::min((long long)c->n_sm, room) / grid) : 1;
+  p.ws = a.ws;
+  p.arrived = a.arrived;
   cudaError_t e;
   if (a.dim == 128)
-    e = fp8 ? launch_attn_prefill<128, true>(s, (int)grid, qm, km, vm, p)
-            : launch_attn_prefill<128, false>(s, (int)grid, qm, km, vm, p);
+    e = fp8 ? launch_attn_prefill<128, true>(s, (int)grid * p.max_split, qm, km, vm, p)
+            : launch_attn_prefill<128, false>(s, (int)grid * p.max_split, qm, km, vm, p);
   else
-    e = fp8 ? launch_attn_prefill<64, true>(s, (int)grid, qm, km, vm, p)
-            : launch_attn_prefill<64, false>(s, (int)grid, qm, km, vm, p);
+    e = fp8 ? launch_attn_prefill<64, true>(s, (int)grid * p.max_split, qm, km, vm, p)
+            : launch_attn_prefill<64, false>(s, (int)grid * p.max_split, qm, km, vm, p);
   CUDA_TRY(c, e);
   return MOE_OK;
 }
 
 moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_stride, int max_T, float scale,
-                  int window, int n_sink, void *out, int64_t out_stride, void *stream, bool chunk, const char *who) {
+                  int window, int n_sink, void *out, int64_t out_stride, void *stream, const char *who) {
   moe_status st = attn_check(c, b, who);
   if (st != MOE_OK) return st;
   if (!b) return fail(c, MOE_ERR_INVALID_ARG, "%s: no batch", who);
@@ -238,11 +245,11 @@ moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_st
   if (!rows_ok(q, q_stride, width, 16) || !rows_ok(out, out_stride, width, 16))
     return fail(c, MOE_ERR_INVALID_ARG, "%s: q and out rows are 16-byte aligned, at least n_q * head_dim apart", who);
   c->last_stream = (cudaStream_t)stream;
-  // Few rows cannot give the chunk kernel's blocks of 256 rows to enough SMs,
-  // while the window kernel splits their keys over all of them: 128 rows of 16
-  // heads of 128 over 16384 keys take 99 us there, against 244 us; 512 rows
-  // 320 us, against 245 us.
-  if (chunk && (long long)b->n_rows * a.n_q > 10 * kApRows)
+  // More rows of a KV head than one row block of the window kernel: 33 rows of
+  // 16 heads over 2 KV heads behind 16384 keys take 48 us in the chunk kernel,
+  // 64 us there; 128 rows 53 us and 99 us.  (max_T is the caller's word; the
+  // window kernel takes more rows than it says in further row blocks.)
+  if ((long long)max_T * (a.n_q / a.n_kv) > kAtMaxRows)
     return attend_chunk(c, b, q, q_stride, scale, window, n_sink, out, out_stride, (cudaStream_t)stream, who);
   CUtensorMap km, vm;
   const int box = a.page < kAtTile ? a.page : kAtTile;
@@ -410,13 +417,13 @@ moe_status moe_attn_forward(moe_ctx *c, const moe_kv_batch *b, const void *q, in
   if (max_T > kDecMaxT)
     return fail(c, MOE_ERR_INVALID_ARG, "moe_attn_forward: max_T=%d, at most %d (moe_attn_prefill takes chunks)", max_T,
                 kDecMaxT);
-  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, false, "moe_attn_forward");
+  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, "moe_attn_forward");
 }
 
 moe_status moe_attn_prefill(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_stride, int max_T,
                             float scale, int window, int n_sink, void *out, int64_t out_stride, void *stream) {
   if (!c) return MOE_ERR_INVALID_ARG;
-  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, true, "moe_attn_prefill");
+  return attend(c, b, q, q_stride, max_T, scale, window, n_sink, out, out_stride, stream, "moe_attn_prefill");
 }
 
 }  // extern "C"

@@ -78,8 +78,20 @@ struct AttnPfParams {
   int window, n_sink;
   int n_rows, n_q, n_kv, group, pack, pack_shift;
   int n_pages, n_seqs, max_pages, page, page_shift;
+  int bases, max_split;    // blocks before splitting their keys, and parts of one at most
+  float *ws;               // [bases][max_split]: a part's rows, see the end of the kernel
+  unsigned int *arrived;   // [bases], zero between calls
   int *status;
 };
+
+// Parts that a block's n key tiles are cut into when there are few blocks: at
+// least four tiles each, and no more than pay for their joining (a tile takes
+// about 2 us, a part about 1 us of the join).
+MOE_HOST_DEV_INLINE int key_parts(int n, int most) {
+  int k = 1;
+  while (k < most && n >= 4 * (k + 1) && (k + 1) * (k + 1) <= 2 * n) ++k;
+  return k;
+}
 
 struct AttnPfShared {
   unsigned long long q_full, kv_full[4], kv_empty[4], s_full[2], p_full[2][2], o_full[2], turn[2], edge, drain[2];
@@ -87,7 +99,7 @@ struct AttnPfShared {
   long long scan[16];
   uint32_t tmem;
   int item[2];  // sequence, row block
-  int dead;
+  int dead, last;
 };
 static_assert(sizeof(AttnPfShared) <= 1024, "fits the block before the tiles");
 
@@ -187,7 +199,8 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
   // ---- this block's item: head group fastest (blocks that share keys run
   // together), then row blocks from the sequence's last (the longest) back
   const int n_hg = p.n_q >> p.pack_shift;
-  const int hg = blockIdx.x % n_hg, item = blockIdx.x / n_hg;
+  const int base = blockIdx.x % p.bases, part = blockIdx.x / p.bases;
+  const int hg = base % n_hg, item = base / n_hg;
   const int tokens = kApRows >> p.pack_shift;  // of a block
   const int per = (p.n_seqs + kApThreads - 1) / kApThreads;
   const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
@@ -268,6 +281,14 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
   sv.rows = t_hi - t_lo;
   sv.kv = pos0 + t_hi;
   const SeqTiles tl = seq_tiles(sv, p.window, p.n_sink, kApTile);
+  // this part's tiles
+  const int parts = key_parts(tl.n, p.max_split);
+  if (part >= parts) {  // block-uniform
+    if (wid == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    return;
+  }
+  const int j_lo = (int)((long long)tl.n * part / parts), n_tiles = (int)((long long)tl.n * (part + 1) / parts) - j_lo;
+  auto key_of = [&](int j) { return tile_at_lead_last(tl, j_lo + j) * kApTile; };
   auto give_up = [&]() {
     *reinterpret_cast<volatile int *>(&sh.dead) = 1;
     atomicOr(p.status, kErrTimeout);
@@ -296,7 +317,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     // this lane's box of tile j: whether its page holds a key that is seen,
     // and its row in the cache
     auto box_of = [&](int j, bool &need, int &y) {
-      const int key0 = tile_at_lead_last(tl, j) * kApTile, pg0 = key0 >> p.page_shift;
+      const int key0 = key_of(j), pg0 = key0 >> p.page_shift;
       if (pg0 < held_at || pg0 + ppt > held_at + 32) {
         held = pg0 == held_at + 32 ? ahead : entries(pg0);
         held_at = pg0;
@@ -330,7 +351,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       }
       bool need = false;
       int y = 0, issued = 0;
-      for (int i = 0; i < 2 * tl.n; ++i) {
+      for (int i = 0; i < 2 * n_tiles; ++i) {
         if (!(i & 1)) box_of(i >> 1, need, y);
         const int st = i & 1, use = i >> 1;
         const uint32_t bytes = bytes_of(need), bar = smem_addr(&sh.raw_full[st]);
@@ -358,10 +379,10 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     __syncwarp();
     if (need) tma_load_2d(kfirst + box_at, &kmap, my_half * 64, y, q_bar);
     int issued = 0, edge_uses = 0;
-    for (int j = 0; j < tl.n; ++j) {
-      const int key0 = tile_at_lead_last(tl, j) * kApTile;
+    for (int j = 0; j < n_tiles; ++j) {
+      const int key0 = key_of(j);
       need_k = false;
-      if (j + 1 < tl.n) box_of(j + 1, need_k, y_k);
+      if (j + 1 < n_tiles) box_of(j + 1, need_k, y_k);
       const int st = j % C::PAIRS, use = j / C::PAIRS;
       const bool edge = key0 + kApTile > s.kv || (key0 < seen_lo && key0 + kApTile > sink_end);
       const uint32_t bytes_v = bytes_of(need), bytes_k = bytes_of(need_k);
@@ -433,7 +454,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
         if (FP8) umma_commit(smem_addr(&sh.kv_empty[C::PAIRS - 1]));  // the first keys' place
         if (t == 1) mbar_arrive(smem_addr(&sh.turn[0]));
       }
-      for (int j = 0; j < tl.n && ok; ++j) {
+      for (int j = 0; j < n_tiles && ok; ++j) {
         const int st = j % C::PAIRS;
         const uint32_t va = slot0 + st * 2 * C::TILE;
         ok = mbar_wait_live(smem_addr(&sh.kv_full[st]), (j / C::PAIRS) & 1, &sh.dead) &&
@@ -449,7 +470,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
         }
         if (!ok) break;
         // in order behind the product that reads P, whose columns it overwrites
-        if (j + 1 < tl.n) scores(va + C::TILE);
+        if (j + 1 < n_tiles) scores(va + C::TILE);
         else umma_commit(smem_addr(&sh.o_full[t]));
         mbar_arrive(smem_addr(&sh.turn[t ^ 1]));
         umma_commit(smem_addr(&sh.kv_empty[st]));
@@ -469,10 +490,10 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     few_registers();
     const int c16 = tid % (D / 16);  // this lane's 16 columns
     bool ok = true;
-    for (int i = 0; i <= 2 * tl.n && ok; ++i) {
+    for (int i = 0; i <= 2 * n_tiles && ok; ++i) {
       // tile i: key tile i / 2, or value tile i / 2; key tile n does not exist
       const int j = i >> 1, st = i & 1;
-      const bool is_v = i & 1, there = i < 2 * tl.n;
+      const bool is_v = i & 1, there = i < 2 * n_tiles;
       const int pair = i == 0 ? C::PAIRS - 1 : (is_v ? j : j - 1) % C::PAIRS;
       const uint32_t dst = slot0 + (2 * pair + (is_v ? 0 : 1)) * C::TILE;
       if (is_v) {  // the pair's place is free (the last pair's held the first keys)
@@ -482,7 +503,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       if (there && ok) {
         ok = mbar_wait_warp(smem_addr(&sh.raw_full[st]), j & 1, &sh.dead);
         if (ok) {
-          const int key0 = tile_at_lead_last(tl, j) * kApTile;
+          const int key0 = key_of(j);
           const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < seen_lo && key0 + kApTile > sink_end));
 #pragma unroll 2
           for (int r = (tid & 127) / (D / 16); r < kApTile; r += 128 / (D / 16)) {
@@ -528,8 +549,8 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * D;
     float m_ref = -INFINITY, l_run = 0.f;  // m_ref in units of the scores times scale_log2
     bool ok = true;
-    for (int j = 0; j < tl.n; ++j) {
-      const int key0 = tile_at_lead_last(tl, j) * kApTile;
+    for (int j = 0; j < n_tiles; ++j) {
+      const int key0 = key_of(j);
       // visible columns: c <= hi by position; with a window c >= lo or c < sk
       const int hi = pos - key0;
       const int lo = p.window > 0 ? (int)max(0LL, (long long)hi - p.window + 1) : 0;
@@ -612,30 +633,91 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       l_run += sum0 + sum1;
     }
     if (ok) ok = mbar_wait_warp(smem_addr(&sh.o_full[t]), 0, &sh.dead);
-    if (ok) {
-      tc_fence_after();
-      const float vs = FP8 && p.v_scale ? __ldg(p.v_scale + kv_h) : 1.f;
-      const float inv = l_run > 0.f || l_run != l_run ? vs / l_run : 0.f;
-      uint16_t *dst = p.out + (long long)(s.row0 + tok) * p.out_stride + (long long)head * D;
+    const float vs = FP8 && p.v_scale ? __ldg(p.v_scale + kv_h) : 1.f;
+    uint16_t *dst = p.out + (long long)(s.row0 + tok) * p.out_stride + (long long)head * D;
+    auto store = [&](int c, const float (&v)[32]) {  // 32 columns of the row
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32_issue(o_at + c * 32, o);
-        tmem_ld32_wait(o);
-        if (mine_ok) {
+      for (int e = 0; e < 32; e += 8)
+        *reinterpret_cast<uint4 *>(dst + c * 32 + e) = make_uint4(
+            pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]), pack_bf16(v[e + 4], v[e + 5]),
+            pack_bf16(v[e + 6], v[e + 7]));
+    };
+    if (!ok && lane == 0) give_up();
+    if (parts == 1) {
+      if (ok) {
+        tc_fence_after();
+        const float inv = l_run > 0.f || l_run != l_run ? vs / l_run : 0.f;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 v;
-            v.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-            v.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            v.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-            v.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-            *reinterpret_cast<uint4 *>(dst + c * 32 + e) = v;
-          }
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          tmem_ld32(o_at + c * 32, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= inv;
+          if (mine_ok) store(c, v);
         }
       }
-    } else if (lane == 0) {
-      give_up();
+    } else {
+      // A part's rows: o as [D / 4][256 rows] groups of four columns, then the
+      // references and the sums.  The last part to arrive adds them up, in
+      // their order.
+      constexpr int PART = kApRows * (D + 2);
+      const int rr = t * 128 + row;
+      float *const all = p.ws + (long long)base * p.max_split * PART;
+      if (ok) {
+        tc_fence_after();
+        float *w = all + (long long)part * PART;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          tmem_ld32(o_at + c * 32, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4 *>(w + ((c * 8 + e) * kApRows + rr) * 4) =
+                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+        w[kApRows * D + rr] = m_ref;
+        w[kApRows * (D + 1) + rr] = l_run;
+      }
+      bar_sync_n(1, 256);
+      if (tid == 0) {
+        __threadfence();  // the block's part before its arrival, and every part before the join
+        sh.last = atomicAdd(p.arrived + base, 1u) == (unsigned)parts - 1;
+        if (sh.last) p.arrived[base] = 0;
+        __threadfence();
+      }
+      bar_sync_n(1, 256);
+      if (sh.last && mine_ok) {
+        float mx = -INFINITY;
+        for (int i = 0; i < parts; ++i) mx = fmaxf(mx, __ldcg(all + (long long)i * PART + kApRows * D + rr));
+        const float mu = mx == -INFINITY ? 0.f : mx;
+        float acc[D / 32][32], l = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[c][e] = 0.f;
+        for (int i = 0; i < parts; ++i) {
+          const float *w = all + (long long)i * PART;
+          const float f = ex2(__ldcg(w + kApRows * D + rr) - mu);
+          l += f * __ldcg(w + kApRows * (D + 1) + rr);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = ldcg_f4(w + ((c * 8 + e) * kApRows + rr) * 4);
+              acc[c][4 * e] += f * v.x;
+              acc[c][4 * e + 1] += f * v.y;
+              acc[c][4 * e + 2] += f * v.z;
+              acc[c][4 * e + 3] += f * v.w;
+            }
+        }
+        const float inv = l > 0.f || l != l ? vs / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) acc[c][e] *= inv;
+          store(c, acc[c]);
+        }
+      }
     }
   }
   tc_fence_before();

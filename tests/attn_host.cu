@@ -6,7 +6,10 @@
 #include <set>
 #include <vector>
 
-#include "attn.cuh"
+#include <algorithm>
+
+#include "../include/moe.h"
+#include "attn_prefill.cuh"
 
 using namespace moe;
 
@@ -105,7 +108,24 @@ static void runs() {
       }
 }
 
+// The parts of a block's tiles: none empty, together all, no more than asked.
+static void key_ranges() {
+  for (int n = 1; n < 3000; n = n < 300 ? n + 1 : n * 2)
+    for (int most : {1, 2, 3, 7, 37, 148}) {
+      const int k = key_parts(n, most);
+      CHECK(k >= 1 && k <= most);
+      int at = 0;
+      for (int i = 0; i < k; ++i) {
+        const int lo = (int)((long long)n * i / k), hi = (int)((long long)n * (i + 1) / k);
+        CHECK(lo == at && hi > lo);
+        at = hi;
+      }
+      CHECK(at == n);
+    }
+}
+
 int main() {
+  key_ranges();
   tiles();
   tables();
   runs();

@@ -211,7 +211,7 @@ def run_attention(B, make_ctx, fn, e4m3, rows, kv, page, n_q, n_kv, dim, window,
     batch = cache.batch(B, rows, extra)
     fn(ctx, batch, q, max(rows), scale, window, sinks, out)
     B.moe_sync(ctx, 60000)
-    want, tol = A.attention64(q[:n], cache, rows, scale, window, sinks, chunk=fn is B.moe_attn_prefill)
+    want, tol = A.attention64(q[:n], cache, rows, scale, window, sinks, chunk=max(rows) * (n_q // n_kv) > 64)
     close(out[:n], want, tol)
     assert (out[n:] == 3).all()
     # the same call again gives the same bits, and so does out = q
@@ -233,6 +233,21 @@ def test_forward_peaked_and_flat_scores(B, make_ctx):
         out = torch.empty_like(q)
         B.moe_attn_forward(ctx, batch, q, 2, 1 / math.sqrt(128), 0, 0, out)
         want, tol = A.attention64(q, cache, [2], 1 / math.sqrt(128), 0, 0)
+        close(out, want, tol)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_more_rows_than_announced(B, make_ctx, e4m3):
+    """max_T below a sequence's rows: the same results, in more row blocks."""
+    ctx = make_ctx(16, 2, 128, 64, e4m3)
+    rows = [20, 1, 41]
+    cache = A.Cache([500, 90, 41], 2, 128, 64, e4m3, seed=3)
+    q = rnd((sum(rows), 16, 128), 4, scale=2.0)
+    out = torch.empty_like(q)
+    for fn in (B.moe_attn_forward, B.moe_attn_prefill):
+        out.fill_(float("nan"))
+        fn(ctx, cache.batch(B, rows), q, 1, 0.09, 100, 3, out)
+        want, tol = A.attention64(q, cache, rows, 0.09, 100, 3)
         close(out, want, tol)
 
 
@@ -398,6 +413,9 @@ CHUNKS = [
     ([300], [900], 16, 16, 16, 128, 0, 0),          # one head per tile
     ([2000], [2500], 128, 3, 1, 64, 90, 5),
     ([520, 0, 1], [520, 0, 700], 16, 8, 2, 64, 0, 0),
+    ([50], [9000], 64, 8, 2, 128, 0, 0),            # few blocks: their keys split over the SMs
+    ([65, 33], [5000, 3333], 32, 12, 2, 64, 3000, 100),
+    ([90], [20000], 128, 4, 1, 128, 0, 0),
     ([40] * 50, [40 + i for i in range(50)], 16, 16, 2, 64, 30, 1),  # more than 32 sequences
 ]
 CHUNKS = [(r, [max(a, b) for a, b in zip(r, k)], *rest) for r, k, *rest in CHUNKS]

@@ -82,7 +82,7 @@ class Decoder:
         view = SimpleNamespace(n_kv=N_KV, e4m3=kv.k[0].dtype == A.E4M3, kv=kv.length, rows64=rows64)
         n = sum(kv.rows)
         want, tol = A.attention64(qkv[:n, :N_Q].contiguous(), view, kv.rows, DIM ** -0.5, kv.window, kv.n_sink,
-                                  chunk=kv.most_rows > 32)
+                                  chunk=kv.most_rows * (N_Q // N_KV) > 64)
         over = (out[:n].double() - want).abs() - tol
         assert torch.isfinite(out[:n]).all() and over.max() <= 0, float(over.max())
 
