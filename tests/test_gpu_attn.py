@@ -446,3 +446,103 @@ def test_scores_that_keep_growing(B, make_ctx, e4m3, rows):
         want, tol = A.attention64(q, cache, [rows], 1 / math.sqrt(128), 0, 0, chunk=rows > 32)
         close(out, want, tol)
     B.moe_sync(ctx, 60000)
+
+
+@pytest.mark.parametrize("rows,window", [(1, 0), (3, 40), (70, 0)])
+def test_hundreds_of_sequences(B, make_ctx, rows, window):
+    """More sequences than a block has threads: every thread holds several."""
+    n = 700 if rows < 10 else 400
+    counts = [(i * 7) % (rows + 1) for i in range(n)]
+    kv = [max(c, 1 + (i * 37) % 90) for i, c in enumerate(counts)]
+    run_attention(B, make_ctx, B.moe_attn_prefill if rows > 32 else B.moe_attn_forward, False, counts, kv, 16, 8, 2,
+                  64, window, 2 if window else 0)
+
+
+def test_e4m3_without_scales(B, make_ctx):
+    for rows in (2, 90):
+        ctx = make_ctx(8, 2, 64, 16, True)
+        cache = A.Cache([200], 2, 64, 16, True, seed=3)
+        cache.k_scale = cache.v_scale = None
+        q = rnd((rows, 8, 64), 4)
+        out = torch.empty_like(q)
+        # values of the type's own range: a scale of 1/64 in the softmax's
+        B.moe_attn_prefill(ctx, cache.batch(B, [rows]), q, rows, 0.125 / 64, 0, 0, out)
+        want, tol = A.attention64(q, cache, [rows], 0.125 / 64, 0, 0, chunk=rows * 4 > 64)
+        close(out, want, tol)
+
+
+@pytest.mark.parametrize("rows", [2, 100])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_off_their_lines(B, make_ctx, e4m3, rows):
+    """Rows that begin 16 bytes into a line and end anywhere."""
+    ctx = make_ctx(6, 2, 64, 32, e4m3)
+    cache = A.Cache([rows + 70], 2, 64, 32, e4m3, seed=8)
+    wide = rnd((rows, 6 * 64 + 24), 4, scale=2.0)
+    q = wide[:, 8:8 + 6 * 64]
+    out = torch.full((rows, 6 * 64 + 8), 2.0, dtype=torch.bfloat16, device="cuda")
+    B.moe_attn_prefill(ctx, cache.batch(B, [rows]), q, rows, 0.125, 0, 0, out[:, 8:])
+    want, tol = A.attention64(q.reshape(rows, 6, 64), cache, [rows], 0.125, 0, 0, chunk=rows * 3 > 64)
+    close(out[:, 8:].reshape(rows, 6, 64), want, tol)
+    assert (out[:, :8] == 2).all()
+
+
+def test_split_chunk_replays(B, make_ctx):
+    """A captured chunk whose keys are split over the SMs, replayed with other
+    lengths (other splits), on a stream of its own."""
+    ctx = make_ctx(8, 2, 128, 64, False)
+    cache = A.Cache([6000], 2, 128, 64, False, seed=8)
+    batch = cache.batch(B, [100])
+    q = rnd((100, 8, 128), 4, scale=2.0)
+    out = torch.empty_like(q)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        B.moe_attn_prefill(ctx, batch, q, 100, 0.09, 0, 0, out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.moe_attn_prefill(ctx, batch, q, 100, 0.09, 0, 0, out)
+    for length in (6000, 100, 3001, 6000):
+        batch.tensors[4].fill_(length)
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        cache.kv = [length]
+        want, tol = A.attention64(q, cache, [100], 0.09, 0, 0)
+        close(out, want, tol)
+    B.moe_sync(ctx, 60000)
+
+
+def test_two_contexts_on_two_streams(B, make_ctx):
+    """Calls of two contexts may overlap: each has its own scratch."""
+    work = []
+    for i, (n_kv, kv) in enumerate(((2, 5000), (4, 4000))):
+        ctx = make_ctx(8, n_kv, 128, 64, False)
+        cache = A.Cache([kv], n_kv, 128, 64, False, seed=i)
+        for rows in (2, 60):
+            q = rnd((rows, 8, 128), i + rows, scale=2.0)
+            work.append((ctx, cache, rows, q, torch.empty_like(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for j in (0, 2, 1, 3):
+            ctx, cache, rows, q, out, _ = work[j]
+            s = work[j // 2 * 2][5]  # a stream per context
+            with torch.cuda.stream(s):
+                B.moe_attn_prefill(ctx, cache.batch(B, [rows]), q, rows, 0.09, 0, 0, out)
+    torch.cuda.synchronize()
+    for ctx, cache, rows, q, out, _ in work:
+        want, tol = A.attention64(q, cache, [rows], 0.09, 0, 0)
+        close(out, want, tol)
+
+
+def test_empty_calls(B, make_ctx):
+    ctx = make_ctx(8, 2, 64, 16, False)
+    cache = A.Cache([50, 0], 2, 64, 16, False, seed=9)
+    q, k = rnd((3, 8, 64), 1), rnd((3, 2, 64), 2)
+    out = torch.full_like(q, 5.0)
+    before = cache.k.clone().view(torch.int16)
+    for batch in (cache.batch(B, [0, 0]), cache.batch(B, [0, 0], 3)):
+        B.moe_kv_append(ctx, batch, q, k, k, None, None, out)
+        B.moe_attn_forward(ctx, batch, q, 1, 0.1, 0, 0, out)
+        B.moe_attn_prefill(ctx, batch, q, 100, 0.1, 5, 1, out)
+    B.moe_sync(ctx, 60000)
+    assert (out == 5).all() and torch.equal(cache.k.view(torch.int16), before)
