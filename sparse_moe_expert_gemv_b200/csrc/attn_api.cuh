@@ -40,16 +40,21 @@ moe_status rope_check(moe_ctx *c, const moe_qk_norm *norm, const moe_rope *rope,
   return MOE_OK;
 }
 
-template <int D, int CACHE>
-cudaError_t launch_kv_rows(moe_ctx *c, cudaStream_t s, const KvRowsParams &p) {
-  // A warp per row and eight rows a block once that gives every other SM a
-  // block (8192 rows of 16 + 4 heads of 128: 20.4 us, against 33.9 us with two
-  // rows a block; 1001 rows of 32 + 8 heads of 64: 3.5 us, against 4.1 us with
-  // one row); below, one row a block, its heads over eight warps.
+template <int D, int CACHE, bool INTER>
+cudaError_t launch_kv_rows_as(moe_ctx *c, cudaStream_t s, const KvRowsParams &p) {
+  // A warp per row and four rows a block once that gives every other SM a
+  // block (8192 rows of 16 + 4 heads of 128: 18.2 us, 19.0 us with eight rows
+  // a block, 33.9 us with two of them on eight warps); below, one row a block,
+  // its heads over eight warps (8 windows of 4 rows: 3.3 us, with four warps a
+  // row 3.6 us).
   if (2 * p.n_rows >= kKvRows * c->n_sm)
-    return launch(kv_rows_kernel<D, CACHE, kKvRows>, dim3((p.n_rows + kKvRows - 1) / kKvRows), dim3(kKvThreads), 0, s,
-                  p);
-  return launch(kv_rows_kernel<D, CACHE, 1>, dim3(p.n_rows), dim3(kKvThreads), 0, s, p);
+    return launch(kv_rows_kernel<D, CACHE, kKvRows, INTER>, dim3((p.n_rows + kKvRows - 1) / kKvRows), dim3(kv_threads(kKvRows)), 0,
+                  s, p);
+  return launch(kv_rows_kernel<D, CACHE, 1, INTER>, dim3(p.n_rows), dim3(kv_threads(1)), 0, s, p);
+}
+template <int D, int CACHE>
+cudaError_t launch_kv_rows(moe_ctx *c, cudaStream_t s, const KvRowsParams &p, bool inter) {
+  return inter ? launch_kv_rows_as<D, CACHE, true>(c, s, p) : launch_kv_rows_as<D, CACHE, false>(c, s, p);
 }
 
 moe_status kv_rows(moe_ctx *c, cudaStream_t s, KvRowsParams &p, const moe_qk_norm *norm, const moe_rope *rope,
@@ -67,15 +72,15 @@ moe_status kv_rows(moe_ctx *c, cudaStream_t s, KvRowsParams &p, const moe_qk_nor
   if (rope) {
     p.inv_freq = rope->inv_freq;
     p.rot = rope->rot_dim;
-    p.interleaved = rope->interleaved;
   }
+  const bool in = rope && rope->interleaved;
   cudaError_t e;
   if (c->attn.dim == 128)
-    e = cache == 0 ? launch_kv_rows<128, 0>(c, s, p)
-                   : cache == 1 ? launch_kv_rows<128, 1>(c, s, p) : launch_kv_rows<128, 2>(c, s, p);
+    e = cache == 0 ? launch_kv_rows<128, 0>(c, s, p, in)
+                   : cache == 1 ? launch_kv_rows<128, 1>(c, s, p, in) : launch_kv_rows<128, 2>(c, s, p, in);
   else
-    e = cache == 0 ? launch_kv_rows<64, 0>(c, s, p)
-                   : cache == 1 ? launch_kv_rows<64, 1>(c, s, p) : launch_kv_rows<64, 2>(c, s, p);
+    e = cache == 0 ? launch_kv_rows<64, 0>(c, s, p, in)
+                   : cache == 1 ? launch_kv_rows<64, 1>(c, s, p, in) : launch_kv_rows<64, 2>(c, s, p, in);
   CUDA_TRY(c, e);
   return MOE_OK;
 }

@@ -144,25 +144,6 @@ MOE_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int
       : "memory");
 }
 
-// Two fp32 values in one register pair: one instruction for both.
-MOE_DEV uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-MOE_DEV void f2_unpack(uint64_t v, float &lo, float &hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-MOE_DEV uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-MOE_DEV uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // P of 32 columns of a row: p = 2^(s scale + neg), as bf16 pairs in w, their
 // sum added to both halves of `sum`.
 MOE_DEV void row_exp2(const uint32_t (&r)[32], uint64_t scale, uint64_t neg, uint32_t (&w)[16], uint64_t &sum) {

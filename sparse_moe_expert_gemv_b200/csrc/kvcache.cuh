@@ -23,8 +23,9 @@
 
 namespace moe {
 
-constexpr int kKvThreads = 256;
-constexpr int kKvRows = 8;      // rows of a block once there are enough of them
+constexpr int kKvRows = 4;  // rows of a block, a warp each, once there are enough of them
+// one row's heads are shared by eight warps
+constexpr int kv_threads(int rows) { return rows == 1 ? 256 : 32 * rows; }
 constexpr int kKvMaxDim = 128;
 
 // A sequence's rows in the call and its cache length, checked: the offsets
@@ -60,7 +61,7 @@ struct KvRowsParams {
   float eps;
   int norm;
   const double *inv_freq;             // [rot / 2] or null
-  int rot, interleaved;
+  int rot;
   int n_rows, n_q, n_kv;
   // cache
   uint8_t *k_cache, *v_cache;         // [n_pages][n_kv][page][D]
@@ -70,32 +71,37 @@ struct KvRowsParams {
   int *status;
 };
 
-MOE_DEV void bf16x4_to_float(uint2 u, float *x) {
-  x[0] = __uint_as_float(u.x << 16);
-  x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(u.y << 16);
-  x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+// two bf16 values as a pair of fp32
+MOE_DEV uint64_t bf16x2_to_f2(uint32_t u) {
+  return f2_pack(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
 MOE_DEV uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-MOE_DEV uint2 float_to_bf16x4(const float *x) {
-  return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+MOE_DEV uint32_t f2_to_bf16x2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16(lo, hi);
 }
-// Four e4m3 values, round to nearest even; finite values past the type's
+// Four e4m3 values of v / scale, round to nearest even; finite values past the type's
 // largest (and infinities) become +-448, NaN stays NaN.
-MOE_DEV uint32_t float_to_e4m3x4(const float *x) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+MOE_DEV uint32_t f2_to_e4m3x4(uint64_t v0, uint64_t v1, float scale) {
+  float2 a, b;
+  f2_unpack(v0, a.x, a.y);
+  f2_unpack(v1, b.x, b.y);
+  a.x /= scale, a.y /= scale, b.x /= scale, b.y /= scale;
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
 
 // CACHE 0: q and k rows to q_out and k_out; 1: q rows to q_out (when given),
 // k and v rows to a bf16 cache; 2: the same with an e4m3 cache.
-template <int D, int CACHE, int ROWS>
-__global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
+template <int D, int CACHE, int ROWS, bool INTER>
+__global__ void __launch_bounds__(kv_threads(ROWS)) kv_rows_kernel(KvRowsParams p) {
+  constexpr int kKvThreads = kv_threads(ROWS);
   constexpr int LPH = D / 8;    // lanes of a head row
   constexpr int HPW = 32 / LPH; // head rows of a warp's step
   constexpr int NW = kKvThreads / 32;
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
   int e0, e1;
   const int half = p.rot / 2;
   const bool turns = p.inv_freq != nullptr && 4 * sub < half;
-  if (turns && !p.interleaved) {
+  if (turns && !INTER) {
     e0 = 4 * sub;
     e1 = e0 + half;
   } else {
@@ -201,61 +207,72 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
   const int pos = s_pos[r];
   if (CACHE && pos < 0) return;  // a row of no sequence: left as it was
   const long long at = CACHE ? s_at[r] : 0;
-  float co[4], si[4];
+  // The lane's four pairs' (cos, sin), laid out for the packed products: half
+  // pairs (a0 a1) and (b0 b1) turn by (c0 c1) and (s0 s1), neighbours (a0 b0)
+  // by (c0 c0) and (-s0 s0).
+  uint64_t co[INTER ? 4 : 2], si[INTER ? 4 : 2];
   if (turns) {
-    const float4 *cs = reinterpret_cast<const float4 *>(&s_cs[r][4 * sub]);  // (cos, sin) of two pairs each
+    const float4 *cs = reinterpret_cast<const float4 *>(&s_cs[r][4 * sub]);
     const float4 c01 = cs[0], c23 = cs[1];
-    co[0] = c01.x, co[1] = c01.z, co[2] = c23.x, co[3] = c23.z;
-    si[0] = c01.y, si[1] = c01.w, si[2] = c23.y, si[3] = c23.w;
+    if (INTER) {
+      co[0] = f2_pack(c01.x, c01.x), co[1] = f2_pack(c01.z, c01.z);
+      co[2] = f2_pack(c23.x, c23.x), co[3] = f2_pack(c23.z, c23.z);
+      si[0] = f2_pack(-c01.y, c01.y), si[1] = f2_pack(-c01.w, c01.w);
+      si[2] = f2_pack(-c23.y, c23.y), si[3] = f2_pack(-c23.w, c23.w);
+    } else {
+      co[0] = f2_pack(c01.x, c01.z), co[1] = f2_pack(c23.x, c23.z);
+      si[0] = f2_pack(c01.y, c01.w), si[1] = f2_pack(c23.y, c23.w);
+    }
   }
   uint16_t *qo_row = p.q_out + row * p.q_out_stride;
   uint16_t *ko_row = CACHE ? nullptr : p.k_out + row * p.k_out_stride - (long long)p.n_q * D;
   const uint32_t lanes = ((1u << LPH) - 1u) << (lane / LPH * LPH);  // the lanes of one head row
   auto finish = [&](int h, uint2 a, uint2 b) {
     const bool is_q = h < p.n_q, is_v = CACHE && h >= p.n_q + p.n_kv;
-    float x[8];
-    bf16x4_to_float(a, x);
-    bf16x4_to_float(b, x + 4);
+    uint64_t x[4] = {bf16x2_to_f2(a.x), bf16x2_to_f2(a.y), bf16x2_to_f2(b.x), bf16x2_to_f2(b.y)};
     if (!is_v) {
       if (p.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+        const uint64_t sq = f2_fma(x[0], x[0], f2_fma(x[1], x[1], f2_fma(x[2], x[2], f2_mul(x[3], x[3]))));
+        float ss, s1;
+        f2_unpack(sq, ss, s1);
+        ss += s1;
 #pragma unroll
         for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
         const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+        const uint64_t inv2 = f2_pack(inv, inv);
         const float *g = is_q ? p.q_gamma : p.k_gamma;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], inv2);
         if (g) {
-          const float4 ga = __ldg(reinterpret_cast<const float4 *>(g + e0));
-          const float4 gb = __ldg(reinterpret_cast<const float4 *>(g + e1));
-          const float gg[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * gg[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= inv;
+          const ulonglong2 ga = __ldg(reinterpret_cast<const ulonglong2 *>(g + e0));
+          const ulonglong2 gb = __ldg(reinterpret_cast<const ulonglong2 *>(g + e1));
+          x[0] = f2_mul(x[0], ga.x), x[1] = f2_mul(x[1], ga.y);
+          x[2] = f2_mul(x[2], gb.x), x[3] = f2_mul(x[3], gb.y);
         }
       }
       if (turns) {
-        // pairs (i, 4 + i) of the lane's elements, or (2 i, 2 i + 1)
-        float y[8];
+        if (INTER) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = p.interleaved ? x[2 * i] : x[i], w = p.interleaved ? x[2 * i + 1] : x[4 + i];
-          y[i] = u * co[i] - w * si[i];
-          y[4 + i] = w * co[i] + u * si[i];
-        }
+          for (int i = 0; i < 4; ++i) {
+            float u, w;
+            f2_unpack(x[i], u, w);
+            x[i] = f2_fma(x[i], co[i], f2_mul(f2_pack(w, u), si[i]));
+          }
+        } else {
+          const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = p.interleaved ? y[(i & 1) * 4 + i / 2] : y[i];
-          x[4 + i] = p.interleaved ? y[(i & 1) * 4 + 2 + i / 2] : y[4 + i];
+          for (int i = 0; i < 2; ++i) {
+            const uint64_t u = x[i], w = x[2 + i];
+            x[i] = f2_fma(u, co[i], f2_mul(f2_mul(w, minus), si[i]));
+            x[2 + i] = f2_fma(w, co[i], f2_mul(u, si[i]));
+          }
         }
       }
     }
     if (is_q || !CACHE) {
       uint16_t *dst = (is_q ? qo_row : ko_row) + (long long)h * D;
-      *reinterpret_cast<uint2 *>(dst + e0) = float_to_bf16x4(x);
-      *reinterpret_cast<uint2 *>(dst + e1) = float_to_bf16x4(x + 4);
+      *reinterpret_cast<uint2 *>(dst + e0) = make_uint2(f2_to_bf16x2(x[0]), f2_to_bf16x2(x[1]));
+      *reinterpret_cast<uint2 *>(dst + e1) = make_uint2(f2_to_bf16x2(x[2]), f2_to_bf16x2(x[3]));
       return;
     }
     if (!CACHE || at < 0) return;
@@ -263,21 +280,19 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(KvRowsParams p) {
     const long long to = (at + (long long)kh * p.page) * D;
     if (CACHE == 2) {
       const float *scale = is_v ? p.v_scale : p.k_scale;
-      if (scale) {
-        const float s = __ldg(scale + kh);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] / s;
-      }
+      const float by = scale ? __ldg(scale + kh) : 1.f;
       uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + to;
-      *reinterpret_cast<uint32_t *>(dst + e0) = float_to_e4m3x4(x);
-      *reinterpret_cast<uint32_t *>(dst + e1) = float_to_e4m3x4(x + 4);
+      *reinterpret_cast<uint32_t *>(dst + e0) = f2_to_e4m3x4(x[0], x[1], by);
+      *reinterpret_cast<uint32_t *>(dst + e1) = f2_to_e4m3x4(x[2], x[3], by);
     } else {
       uint16_t *dst = reinterpret_cast<uint16_t *>(is_v ? p.v_cache : p.k_cache) + to;
-      *reinterpret_cast<uint2 *>(dst + e0) = float_to_bf16x4(x);
-      *reinterpret_cast<uint2 *>(dst + e1) = float_to_bf16x4(x + 4);
+      *reinterpret_cast<uint2 *>(dst + e0) = make_uint2(f2_to_bf16x2(x[0]), f2_to_bf16x2(x[1]));
+      *reinterpret_cast<uint2 *>(dst + e1) = make_uint2(f2_to_bf16x2(x[2]), f2_to_bf16x2(x[3]));
     }
   };
-  // the next heads' loads go out before the present ones are finished
+  // the next heads' loads go out before the present ones are finished (PRE
+  // heads a round: 19.0 us for 8192 rows of 16 + 4 heads of 128; reloading each
+  // head's registers as it is finished: 22.3 us)
   for (; h < heads; h += PRE * step) {
     uint2 ya[PRE], yb[PRE];
 #pragma unroll
