@@ -793,10 +793,17 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         for (int i = 0; i < 2; ++i) {
           const int r = mt * 16 + g + 8 * i;
           if (!row_ok[i]) continue;
+          float *row = w + r * D;
+          if (FP8) {
 #pragma unroll
-          for (int n = 0; n < ND; ++n)
+            for (int n = 0; n < ND; n += 2)
+              *reinterpret_cast<float4 *>(row + col_of(n, 0)) =
+                  make_float4(o[n][2 * i], o[n + 1][2 * i], o[n][2 * i + 1], o[n + 1][2 * i + 1]);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) w[(long long)r * D + col_of(n, e)] = o[n][2 * i + e];
+            for (int n = 0; n < ND; ++n)
+              *reinterpret_cast<float2 *>(row + col_of(n, 0)) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+          }
           if (cq == 0) {
             w[RB * D + r] = m_run[i];
             w[RB * D + RB + r] = l_run[i];
@@ -808,8 +815,10 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         const unsigned int parts = lastb - first + 1;
         __threadfence();  // the block's part before its arrival, and every part before the join
         sh.last = atomicAdd(p.arrived + first, 1u) == parts - 1;
-        if (sh.last) p.arrived[first] = 0;
-        __threadfence();
+        if (sh.last) {
+          p.arrived[first] = 0;
+          __threadfence();
+        }
       }
       bar_sync_n(1, kAtWarps * 32);
       if (sh.last) {
