@@ -628,13 +628,35 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       if (ok) {
         tc_fence_after();
         const float inv = l_run > 0.f || l_run != l_run ? vs / l_run : 0.f;
+        // Each warp turns its 32 rows in the place of its queries (every
+        // product that reads them is through), so that whole rows leave at a
+        // time: a thread's own row in 16-byte pieces would touch 32 lines a
+        // store.  A row's pieces are swizzled by the row.
+        constexpr int PIECES = D / 8;
+        const uint32_t mine = q0 + t * C::TILE + (wid & 3) * 32 * D * 2;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
           tmem_ld32(o_at + c * 32, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= inv;
-          if (mine_ok) store(c, v);
+          for (int e = 0; e < 4; ++e)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(mine + lane * D * 2 +
+                                                                       (((c * 4 + e) ^ (lane & 7)) << 4)),
+                         "r"(pack_bf16(v[8 * e] * inv, v[8 * e + 1] * inv)),
+                         "r"(pack_bf16(v[8 * e + 2] * inv, v[8 * e + 3] * inv)),
+                         "r"(pack_bf16(v[8 * e + 4] * inv, v[8 * e + 5] * inv)),
+                         "r"(pack_bf16(v[8 * e + 6] * inv, v[8 * e + 7] * inv))
+                         : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const int at = i * 32 + lane, r = at / PIECES, piece = at % PIECES;
+          const int rr = (wid & 3) * 32 + r, tk = t_lo + t * (tokens / 2) + (rr >> p.pack_shift);
+          const uint4 v = lds_u4(mine + r * D * 2 + ((piece ^ (r & 7)) << 4));
+          if (tk < t_hi)
+            *reinterpret_cast<uint4 *>(p.out + (long long)(s.row0 + tk) * p.out_stride +
+                                       (long long)((hg << p.pack_shift) + (rr & (p.pack - 1))) * D + piece * 8) = v;
         }
       }
     } else {
