@@ -215,23 +215,22 @@ moe_status attend_chunk(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_
   if (!encode_q_map(&qm, a, q, b->n_rows, q_stride, p.pack) || !encode_cache_map(&km, a, b->k, b->n_pages, box, !fp8) ||
       !encode_cache_map(&vm, a, b->v, b->n_pages, box, !fp8))
     return fail(c, MOE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  // the row blocks of all sequences are at most this many (the rest leave at once)
-  const long long blocks = (long long)b->n_rows / (kApRows / p.pack) + b->n_seqs, grid = blocks * (a.n_q / p.pack);
+  // the row blocks of all sequences are at most this many, and their parts at
+  // most one wave more (the rest leave at once); the workspace has room for a
+  // part of 256 rows an SM
+  p.n_sm = (int)std::min<long long>(c->n_sm, (long long)a.grid * 2 * kAtMaxRows / kApRows);
+  const long long blocks = (long long)b->n_rows / (kApRows / p.pack) + b->n_seqs;
+  const long long grid = blocks * (a.n_q / p.pack) + p.n_sm;
   if (grid > 0x7fffffffLL) return fail(c, MOE_ERR_NOT_SUPPORTED, "%s: %lld blocks", who, grid);
-  // few blocks: the spare SMs take parts of their keys (the workspace has room
-  // for n_sm parts of 256 rows)
-  p.bases = (int)grid;
-  const long long room = (long long)a.grid * 2 * kAtMaxRows / kApRows;
-  p.max_split = grid <= 0x7fffffff / 2 ? (int)std::max(1LL, std::min((long long)c->n_sm, room) / grid) : 1;
   p.ws = a.ws;
   p.arrived = a.arrived;
   cudaError_t e;
   if (a.dim == 128)
-    e = fp8 ? launch_attn_prefill<128, true>(s, (int)grid * p.max_split, qm, km, vm, p)
-            : launch_attn_prefill<128, false>(s, (int)grid * p.max_split, qm, km, vm, p);
+    e = fp8 ? launch_attn_prefill<128, true>(s, (int)grid, qm, km, vm, p)
+            : launch_attn_prefill<128, false>(s, (int)grid, qm, km, vm, p);
   else
-    e = fp8 ? launch_attn_prefill<64, true>(s, (int)grid * p.max_split, qm, km, vm, p)
-            : launch_attn_prefill<64, false>(s, (int)grid * p.max_split, qm, km, vm, p);
+    e = fp8 ? launch_attn_prefill<64, true>(s, (int)grid, qm, km, vm, p)
+            : launch_attn_prefill<64, false>(s, (int)grid, qm, km, vm, p);
   CUDA_TRY(c, e);
   return MOE_OK;
 }

@@ -78,15 +78,15 @@ struct AttnPfParams {
   int window, n_sink;
   int n_rows, n_q, n_kv, group, pack, pack_shift;
   int n_pages, n_seqs, max_pages, page, page_shift;
-  int bases, max_split;    // blocks before splitting their keys, and parts of one at most
-  float *ws;               // [bases][max_split]: a part's rows, see the end of the kernel
-  unsigned int *arrived;   // [bases], zero between calls
+  int n_sm;                // blocks that run at once (and parts that the workspace holds)
+  float *ws;               // [n_sm]: a part's rows, see the end of the kernel
+  unsigned int *arrived;   // [n_sm], zero between calls
   int *status;
 };
 
-// Parts that a block's n key tiles are cut into when there are few blocks: at
-// least four tiles each, and no more than pay for their joining (a tile takes
-// about 2 us, a part about 1 us of the join).
+// Parts that a block's n key tiles are cut into when it is one of the last
+// few: at least four tiles each, and no more than pay for their joining (a tile
+// takes about 2 us, a part about 1 us of the join).
 MOE_HOST_DEV_INLINE int key_parts(int n, int most) {
   int k = 1;
   while (k < most && n >= 4 * (k + 1) && (k + 1) * (k + 1) <= 2 * n) ++k;
@@ -178,10 +178,10 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
   pdl_wait();
 
   // ---- this block's item: head group fastest (blocks that share keys run
-  // together), then row blocks from the sequence's last (the longest) back
+  // together), then row blocks from the sequence's last (the longest) back.
+  // What is left after whole waves of one block an SM has its keys split over
+  // the SMs: the last `rem` items come in up to n_sm / rem parts.
   const int n_hg = p.n_q >> p.pack_shift;
-  const int base = blockIdx.x % p.bases, part = blockIdx.x / p.bases;
-  const int hg = base % n_hg, item = base / n_hg;
   const int tokens = kApRows >> p.pack_shift;  // of a block
   const int per = (p.n_seqs + kApThreads - 1) / kApThreads;
   const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
@@ -206,18 +206,30 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     if (w < wid) before += sh.scan[w];
     total += sh.scan[w];
   }
-  if (item >= total) return;  // block-uniform: the grid is sized for the most items there can be
+  const long long all = total * n_hg, whole = all / p.n_sm * p.n_sm;
+  const int rem = (int)(all - whole);
+  int tail = -1, part = 0, most = 1;  // index among the last items
+  long long at = blockIdx.x;
+  if (at >= whole) {
+    most = rem ? p.n_sm / rem : 0;
+    const int x = (int)(at - whole);
+    if (x >= rem * most) return;  // block-uniform: the grid is sized for the most blocks there can be
+    part = x / rem;
+    tail = x - part * rem;
+    at = whole + tail;
+  }
+  const int hg = (int)(at % n_hg), item = (int)(at / n_hg);
   inc += before;
   if (item >= inc - mine && item < inc) {
-    long long at = inc - mine;
+    long long from = inc - mine;
     for (int b = b_lo; b < b_hi; ++b) {
       const int n = blocks_of(view(b));
-      if (item < at + n) {
+      if (item < from + n) {
         sh.item[0] = b;
-        sh.item[1] = n - 1 - (int)(item - at);
+        sh.item[1] = n - 1 - (int)(item - from);
         break;
       }
-      at += n;
+      from += n;
     }
   }
   if (tid == 0) {
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
   sv.kv = pos0 + t_hi;
   const SeqTiles tl = seq_tiles(sv, p.window, p.n_sink, kApTile);
   // this part's tiles
-  const int parts = key_parts(tl.n, p.max_split);
+  const int parts = key_parts(tl.n, most);
   if (part >= parts) {  // block-uniform
     if (wid == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     return;
@@ -665,10 +677,10 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       // their order.
       constexpr int PART = kApRows * (D + 2);
       const int rr = t * 128 + row;
-      float *const all = p.ws + (long long)base * p.max_split * PART;
+      float *const parts_at = p.ws + (long long)tail * most * PART;
       if (ok) {
         tc_fence_after();
-        float *w = all + (long long)part * PART;
+        float *w = parts_at + (long long)part * PART;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
@@ -684,14 +696,14 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       bar_sync_n(1, 256);
       if (tid == 0) {
         __threadfence();  // the block's part before its arrival, and every part before the join
-        sh.last = atomicAdd(p.arrived + base, 1u) == (unsigned)parts - 1;
-        if (sh.last) p.arrived[base] = 0;
+        sh.last = atomicAdd(p.arrived + tail, 1u) == (unsigned)parts - 1;
+        if (sh.last) p.arrived[tail] = 0;
         __threadfence();
       }
       bar_sync_n(1, 256);
       if (sh.last && mine_ok) {
         float mx = -INFINITY;
-        for (int i = 0; i < parts; ++i) mx = fmaxf(mx, __ldcg(all + (long long)i * PART + kApRows * D + rr));
+        for (int i = 0; i < parts; ++i) mx = fmaxf(mx, __ldcg(parts_at + (long long)i * PART + kApRows * D + rr));
         const float mu = mx == -INFINITY ? 0.f : mx;
         float acc[D / 32][32], l = 0.f;
 #pragma unroll
@@ -699,7 +711,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) acc[c][e] = 0.f;
         for (int i = 0; i < parts; ++i) {
-          const float *w = all + (long long)i * PART;
+          const float *w = parts_at + (long long)i * PART;
           const float f = ex2(__ldcg(w + kApRows * D + rr) - mu);
           l += f * __ldcg(w + kApRows * (D + 1) + rr);
 #pragma unroll
