@@ -283,7 +283,15 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     total = units;
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    run = run_length(total, gridDim.x, p.min_units);
+    // A part of R rows costs the block that joins it about 0.05 + R / 230 of a
+    // tile's time, so the longest segment's n tiles are cut into runs of at
+    // least sqrt(n (0.05 + R / 256)): both halves of the chain then take about
+    // the same (one window of 8 rows over 32768 keys, 64 rows of a KV head:
+    // 72 us, against 99.5 us with 128 parts a head).
+    const int n_max = __reduce_max_sync(0xffffffffu, t.n);
+    const int r_max = __reduce_max_sync(0xffffffffu, min(s.rows * p.group, RB));
+    run = run_length(total, gridDim.x,
+                     max(p.min_units, __float2int_ru(sqrtf(n_max * (0.05f + r_max * (1.f / 256.f))))));
     // Where a slightly longer run lets every segment have blocks of its own,
     // no block has two parts to hand over.
     const int segs = t.n ? (int)(units / t.n) : 0;
@@ -829,35 +837,53 @@ __global__ void __launch_bounds__(kAtThreads, 2)
           *reinterpret_cast<uint2 *>(dst) =
               make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
         };
-        constexpr int U = 8;  // parts in flight
-        if (parts <= U) {
-          for (int it = tid; it < rows_here * (D / 4); it += kAtWarps * 32) {
-            const int r = it / (D / 4), d4 = it % (D / 4) * 4;
-            float f[U], li[U];
-            float4 v[U];
+        // few parts: U of them for I groups of four columns in flight
+        auto join_few = [&](auto u_, auto i_) {
+          constexpr int U = decltype(u_)::value, I = decltype(i_)::value, STEP = kAtWarps * 32;
+          for (int it0 = tid; it0 < rows_here * (D / 4); it0 += STEP * I) {
+            float f[I][U], li[I][U];
+            float4 v[I][U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-              const float *w = slot_of(first + min(k, parts - 1));
-              f[k] = __ldcg(w + RB * D + r);
-              li[k] = __ldcg(w + RB * D + RB + r);
-              v[k] = ldcg_f4(w + (long long)r * D + d4);
+            for (int i = 0; i < I; ++i) {
+              const int it = min(it0 + i * STEP, rows_here * (D / 4) - 1), r = it / (D / 4), d4 = it % (D / 4) * 4;
+#pragma unroll
+              for (int k = 0; k < U; ++k) {
+                const float *w = slot_of(first + min(k, parts - 1));
+                f[i][k] = __ldcg(w + RB * D + r);
+                li[i][k] = __ldcg(w + RB * D + RB + r);
+                v[i][k] = ldcg_f4(w + r * D + d4);
+              }
             }
-            float mx = f[0];
 #pragma unroll
-            for (int k = 1; k < U; ++k) mx = fmaxf(mx, f[k]);
-            const float mu = mx == -INFINITY ? 0.f : mx;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+            for (int i = 0; i < I; ++i) {
+              const int it = it0 + i * STEP;
+              if (it >= rows_here * (D / 4)) break;
+              float mx = f[i][0];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-              const float e = k < parts ? ex2(f[k] - mu) : 0.f;
-              l += e * li[k];
-              acc[0] += e * v[k].x;
-              acc[1] += e * v[k].y;
-              acc[2] += e * v[k].z;
-              acc[3] += e * v[k].w;
+              for (int k = 1; k < U; ++k) mx = fmaxf(mx, f[i][k]);
+              const float mu = mx == -INFINITY ? 0.f : mx;
+              float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+#pragma unroll
+              for (int k = 0; k < U; ++k) {
+                const float e = k < parts ? ex2(f[i][k] - mu) : 0.f;
+                l += e * li[i][k];
+                acc[0] += e * v[i][k].x;
+                acc[1] += e * v[i][k].y;
+                acc[2] += e * v[i][k].z;
+                acc[3] += e * v[i][k].w;
+              }
+              store(it / (D / 4), it % (D / 4) * 4, acc, l > 0.f || l != l ? vs / l : 0.f);
             }
-            store(r, d4, acc, l > 0.f || l != l ? vs / l : 0.f);
           }
+        };
+        // (with one row tile there are few groups, and registers to lose: one
+        // token over 32768 keys 21.1 us without the first two, 22.1 us with them)
+        if (MT > 1 && parts == 2) {
+          join_few(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+        } else if (MT > 1 && parts <= 4) {
+          join_few(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+        } else if (parts <= 8) {
+          join_few(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
         } else {
           // Each part's weight first, a warp per row (as many rows at once as
           // the join buffer holds weights for), then the weighted sums.

@@ -250,10 +250,17 @@ moe_status attend(moe_ctx *c, const moe_kv_batch *b, const void *q, int64_t q_st
     return fail(c, MOE_ERR_INVALID_ARG, "%s: q and out rows are 16-byte aligned, at least n_q * head_dim apart", who);
   c->last_stream = (cudaStream_t)stream;
   // More rows of a KV head than one row block of the window kernel: 33 rows of
-  // 16 heads over 2 KV heads behind 16384 keys take 48 us in the chunk kernel,
-  // 64 us there; 128 rows 53 us and 99 us.  (max_T is the caller's word; the
-  // window kernel takes more rows than it says in further row blocks.)
-  if ((long long)max_T * (a.n_q / a.n_kv) > kAtMaxRows)
+  // 16 heads over 2 KV heads behind 16384 keys take 45 us in the chunk kernel,
+  // 64 us there; 128 rows 49 us and 99 us.  (max_T is the caller's word; the
+  // window kernel takes more rows than it says in further row blocks.)  With
+  // more than 32 rows its four row tiles leave a warp no others to hide behind,
+  // so a bf16 cache goes to the chunk kernel while its blocks fill at most half
+  // of the SMs: 8 windows of 64 rows over 8000 keys 48 us against 65 us; but 64
+  // windows over up to 4096 keys 71 us against 57 us, and e4m3 tiles, converted
+  // there, 26 us against 23 us for 16 windows of 40 rows over 1000 keys.
+  const long long kv_rows = (long long)max_T * (a.n_q / a.n_kv);
+  const long long chunk_blocks = ((long long)b->n_rows * a.n_q / kApRows / a.n_kv + b->n_seqs) * a.n_kv;
+  if (kv_rows > kAtMaxRows || (kv_rows > 32 && a.cache == MOE_KV_BF16 && 2 * chunk_blocks <= c->n_sm))
     return attend_chunk(c, b, q, q_stride, scale, window, n_sink, out, out_stride, (cudaStream_t)stream, who);
   CUtensorMap km, vm;
   const int box = a.page < kAtTile ? a.page : kAtTile;
