@@ -34,11 +34,12 @@
 // keys -- S read 390, maximum 330, exponentials 1,530 (a warp per scheduler
 // reaches two thirds of the special function unit's rate), hand-over 230, P V
 // and S 990, commit 360 -- of which the tensor cores work 2,048 for the two
-// tiles.  8192 rows of 16 heads over 16384 keys: 839 us, 983 TFLOP/s.
-// Measured and not kept: two warps per row (927 us), scores double-buffered
-// in steps of 64 keys (876 us: an MMA of 64 columns takes as long as one of
-// 128), exponentials on the FMA units by a polynomial (a quarter of them: 872
-// against 853 us, half: 913).
+// tiles.  8192 rows of 16 heads over 16384 keys: 782 us, 1.05 PFLOP/s, the
+// blocks of the last incomplete wave splitting their keys (812 us without).
+// Measured at earlier stages and not kept: two warps per row (927 against 900
+// us), scores double-buffered in steps of 64 keys (876 against 845 us: an MMA
+// of 64 columns takes as long as one of 128), exponentials on the FMA units by
+// a polynomial (a quarter of them: 872 against 853 us, half: 913).
 //
 // Tensor memory: S0, S1 (128 columns each, P over the first 64), O0, O1.
 #pragma once

@@ -14,7 +14,9 @@
 // with D / 8 lanes each, two 8-byte (four-element) pieces per lane placed so
 // that both elements of a pair sit in the same lane.  A warp stays with one
 // row: dealing head rows out across rows cost more in index arithmetic than
-// the arithmetic itself.
+// the arithmetic itself.  8192 rows of 16 + 4 heads of 128: 18.1 us, 4.6 TB/s
+// (70 % of a copy; the instructions, about 100 per 16 elements of a lane, are
+// the rest), with the append's values 22.2 us; four rows 2.6 and 3.3 us.
 #pragma once
 
 #include <cuda_fp8.h>
