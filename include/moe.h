@@ -348,8 +348,9 @@ MOE_API moe_status moe_ep_combine(moe_ctx *ctx, int N, const float *w_dev, const
  * left as they were.  The device checks what it reads: a page id outside
  * [0, n_pages), or offsets and lengths that contradict each other or the
  * sizes given here, index nothing out of range, leave the rows concerned
- * unwritten (or, for a page that is only read, unspecified), and set the
- * device status (moe_sync returns DEVICE). */
+ * unwritten (or, for a page that is only read, unspecified; where offsets
+ * descend, other sequences' rows may stay unwritten too), and set the device
+ * status (moe_sync returns DEVICE). */
 enum { MOE_KV_BF16 = 1, MOE_KV_E4M3 = 2 };
 
 typedef struct {

@@ -213,6 +213,10 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
   long long at = blockIdx.x;
   if (at >= whole) {
     most = rem ? p.n_sm / rem : 0;
+    // Offsets that descend (reported) can make more items than the grid was
+    // sized for: then none is split, or some parts would have no block and
+    // their arrivals stay counted.
+    if (all > (long long)gridDim.x - p.n_sm) most = 1;
     const int x = (int)(at - whole);
     if (x >= rem * most) return;  // block-uniform: the grid is sized for the most blocks there can be
     part = x / rem;

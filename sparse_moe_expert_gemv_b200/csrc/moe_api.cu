@@ -1962,6 +1962,8 @@ moe_status moe_sync(moe_ctx *c, int timeout_ms) {
     CUDA_TRY(c, cudaMemsetAsync(c->dec_bar, 0, c->dec_sync_bytes, c->io));
     CUDA_TRY(c, cudaMemsetAsync(c->ticket, 0, 2 * sizeof(unsigned int), c->io));
   }
+  if (at & kErrTimeout)
+    CUDA_TRY(c, cudaMemsetAsync(c->attn.arrived, 0, (size_t)c->attn.grid * sizeof(unsigned int), c->io));
   CUDA_TRY(c, cudaStreamSynchronize(c->io));
   if (st & kErrBadSlot) return fail(c, MOE_ERR_BAD_SLOT, "device status 0x%x: bad slot", st);
   if (at & kErrBadPage) return fail(c, MOE_ERR_DEVICE, "device status 0x%x: a page id outside the cache", st | at);

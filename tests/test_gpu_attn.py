@@ -345,6 +345,26 @@ def test_bad_tables_are_reported_and_index_nothing(B, make_ctx):
             assert (out[1:3] == 5).all() and (q_out[1:3] == 5).all()
 
 
+def test_descending_offsets_leave_no_parts_counted(B, make_ctx):
+    """Offsets that descend make more row blocks than the call has rows for:
+    reported, and later calls whose keys are split over the SMs are right."""
+    ctx = make_ctx(16, 4, 128, 64, False)
+    bad = A.Cache([4608, 64, 4608], 4, 128, 64, False, seed=21)
+    batch = bad.batch(B, [2560, 0, 2560], extra_rows=-2560)
+    batch.tensors[3].copy_(torch.tensor([0, 2560, 0, 2560], dtype=torch.int32))
+    q = rnd((2560, 16, 128), 1)
+    B.moe_attn_prefill(ctx, batch, q, 2560, 0.1, 0, 0, torch.empty_like(q))
+    with pytest.raises(B.MoeError) as ei:
+        B.moe_sync(ctx, 60000)
+    assert ei.value.status == B.MOE_ERR_DEVICE
+    cache = A.Cache([4000], 4, 128, 64, False, seed=22)
+    q = rnd((50, 16, 128), 2)
+    out = torch.empty_like(q)
+    B.moe_attn_prefill(ctx, cache.batch(B, [50]), q, 50, 0.1, 0, 0, out)
+    B.moe_sync(ctx, 60000)
+    close(out, *A.attention64(q, cache, [50], 0.1, 0, 0, chunk=True))
+
+
 def test_refusals(B, make_ctx):
     ctx = make_ctx(8, 2, 64, 16, False)
     cache = A.Cache([50], 2, 64, 16, False, seed=9)
