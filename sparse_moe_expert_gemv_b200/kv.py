@@ -12,6 +12,8 @@ taken back with ``trim`` (section "Speculative decoding").
 The bookkeeping is plain host code; every step on the GPU is a library call.
 The tables are updated in place, so a CUDA graph that captured ``attend``
 replays for the next step of the same shape.
+``step`` writes them on torch's current stream and waits for that: run
+``attend`` on the same stream, or open a step only when the one before is done.
 """
 from __future__ import annotations
 
