@@ -57,18 +57,12 @@ class PagedKV:
     def free_pages(self):
         return len(self._free)
 
-    def _reclaim(self, s):
-        """Gives back pages that no token from position ``length[s]`` on sees."""
+    def _unseen(self, s):
+        """Places of the pages that no token from position ``length[s]`` on sees."""
         if not self.window:
-            return
-        low = self.length[s] - self.window + 1
-        for i, p in enumerate(self.pages[s]):
-            if (i + 1) * self.page > low:
-                break
-            if p >= 0 and i * self.page >= self.n_sink:
-                self._free.append(p)
-                self.pages[s][i] = -1
-                self._table[s, i] = -1
+            return []
+        whole = min(max(0, self.length[s] - self.window + 1) // self.page, len(self.pages[s]))
+        return [i for i in range(-(-self.n_sink // self.page), whole) if self.pages[s][i] >= 0]
 
     def step(self, rows):
         """Opens a step: rows[s] new tokens of sequence slot s (the batch's
@@ -79,12 +73,19 @@ class PagedKV:
             raise ValueError(f"rows: one count for each of {self.max_seqs} slots")
         if any(n + r > self.max_len for n, r in zip(self.length, rows)):
             raise ValueError(f"a sequence would grow past {self.max_len} tokens")
-        for s in range(self.max_seqs):
-            if rows[s]:
-                self._reclaim(s)
+        # what can be given back is counted before anything changes: a refused
+        # step leaves the one before it open, and a trim of that one brings
+        # tokens back into the window
+        unseen = [self._unseen(s) if rows[s] else [] for s in range(self.max_seqs)]
         need = [max(0, -(-(n + r) // self.page) - len(p)) for n, r, p in zip(self.length, rows, self.pages)]
-        if sum(need) > len(self._free):
-            raise MemoryError(f"{sum(need)} pages needed, {len(self._free)} free")
+        free = len(self._free) + sum(map(len, unseen))
+        if sum(need) > free:
+            raise MemoryError(f"{sum(need)} pages needed, {free} free")
+        for s, places in enumerate(unseen):
+            for i in places:
+                self._free.append(self.pages[s][i])
+                self.pages[s][i] = -1
+                self._table[s, i] = -1
         off = [0]
         for s, r in enumerate(rows):
             for _ in range(need[s]):

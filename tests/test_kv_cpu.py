@@ -65,3 +65,59 @@ def test_window_gives_back_only_what_no_later_token_sees():
         check(kv, 12)
         kv.trim(0, rng.randint(0, r - 1))    # rejected draft tokens
     assert kv.pages[0].count(-1) >= 3
+
+
+def visible(kv, s, rows):
+    """Every key that the last `rows` tokens of slot s see has a page."""
+    return all(kv.pages[s][j // kv.page] >= 0 for i in range(kv.length[s] - rows, kv.length[s])
+               for j in range(i + 1) if i - j < kv.window or j < kv.n_sink)
+
+
+@pytest.mark.parametrize("first,second,refused,back", [
+    ([38, 0], [14, 0], [1, 97], 13),   # other slots' tokens do not fit
+    ([26, 16], [10, 0], [1, 60], 9),
+    ([26, 16], [10, 0], [64, 20], 9),
+])
+def test_refused_step_gives_no_page_back(first, second, refused, back):
+    """A step that finds too few pages changes nothing, so the step before it
+    can still be trimmed: its tokens' windows reach back to pages that the
+    refused one would have given back."""
+    kv = make(n_pages=6, max_seqs=2, max_len=100, window=20)
+    kv.step(first)
+    kv.step(second)
+    before = (sorted(kv._free), list(kv.length), list(kv.rows), [list(p) for p in kv.pages], kv._table.tolist())
+    with pytest.raises(MemoryError):
+        kv.step(refused)
+    assert before == (sorted(kv._free), list(kv.length), list(kv.rows), [list(p) for p in kv.pages],
+                      kv._table.tolist())
+    kv.trim(0, back)
+    kv.step([1, 0])
+    assert visible(kv, 0, 1)
+    check(kv, 6)
+
+
+def test_steps_trims_and_refusals_at_random():
+    rng = random.Random(7)
+    refused = 0
+    for trial in range(40):
+        window, sink = rng.choice([1, 5, 20, 40]), rng.choice([0, 3, 16, 17])
+        kv = make(n_pages=7, max_seqs=2, max_len=200, window=window, n_sink=sink)
+        for _ in range(30):
+            rows = [rng.choice([0, 1, 3, 30]) for _ in range(2)]
+            try:
+                kv.step(rows)
+            except (MemoryError, ValueError):
+                refused += 1
+            else:
+                assert all(visible(kv, s, r) for s, r in enumerate(rows))
+            check_given(kv, 7)
+            s = rng.randrange(2)
+            kv.trim(s, rng.randint(0, max(0, kv.rows[s] - 1)))
+            if rng.random() < 0.1:
+                kv.release(s)
+    assert refused > 20
+
+
+def check_given(kv, n_pages):
+    used = [p for s in kv.pages for p in s if p >= 0]
+    assert sorted(used + kv._free) == list(range(n_pages))
