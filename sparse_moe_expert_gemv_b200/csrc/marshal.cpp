@@ -24,7 +24,7 @@ struct Rows {
   int64_t stride = 0;
 };
 
-// Rows [n, heads, dim] (or [n, heads * dim]) of 16-bit elements on `device`,
+// Rows [n, heads, dim] (or [n, heads * dim]) of bf16 on `device`,
 // dense within a row.  False with a Python error set otherwise.
 bool rows(const char *name, PyObject *o, long n, long heads, long dim, long device, Rows *out) {
   if (!THPVariable_Check(o)) {
@@ -33,7 +33,8 @@ bool rows(const char *name, PyObject *o, long n, long heads, long dim, long devi
   }
   const at::Tensor &t = THPVariable_Unpack(o);
   const int64_t k = t.dim();
-  bool ok = (k == 2 || k == 3) && t.is_cuda() && t.element_size() == 2 && t.size(0) >= n && t.stride(k - 1) == 1;
+  bool ok = (k == 2 || k == 3) && t.is_cuda() && t.scalar_type() == at::kBFloat16 && t.size(0) >= n &&
+            t.stride(k - 1) == 1;
   if (ok)
     ok = k == 3 ? t.size(1) == heads && t.size(2) == dim && (heads == 1 || t.stride(1) == dim)
                 : t.size(1) == heads * dim;
