@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <exception>
 
 #include "../../include/moe.h"
 
@@ -85,6 +86,21 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
   if (n == want) return true;
   PyErr_Format(PyExc_TypeError, "%zd arguments, not %zd", want, n);
   return false;
+}
+
+// A tensor whose sizes or memory are not plain numbers (symbolic, nested,
+// without storage) throws when it is asked for them: a Python error, since
+// nothing may be thrown through the interpreter's C frames.
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t na) {
+  try {
+    return F(self, a, na);
+  } catch (const std::exception &e) {
+    PyErr_Format(PyExc_ValueError, "not a plain CUDA tensor: %s", e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_ValueError, "not a plain CUDA tensor");
+  }
+  return nullptr;
 }
 
 // (n_q, n_kv, dim, device, ctx, n_rows, q, k, pos, norm, rope, q_out, k_out, stream)
@@ -170,9 +186,9 @@ PyObject *set_calls(PyObject *, PyObject *const *a, Py_ssize_t na) {
 }
 
 PyMethodDef methods[] = {
-    {"qk_norm_rope", (PyCFunction)(void *)qk_norm_rope, METH_FASTCALL, nullptr},
-    {"kv_append", (PyCFunction)(void *)kv_append, METH_FASTCALL, nullptr},
-    {"attend", (PyCFunction)(void *)attend, METH_FASTCALL, nullptr},
+    {"qk_norm_rope", (PyCFunction)(void *)guarded<qk_norm_rope>, METH_FASTCALL, nullptr},
+    {"kv_append", (PyCFunction)(void *)guarded<kv_append>, METH_FASTCALL, nullptr},
+    {"attend", (PyCFunction)(void *)guarded<attend>, METH_FASTCALL, nullptr},
     {"set_calls", (PyCFunction)(void *)set_calls, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -83,3 +83,34 @@ def test_rows_are_checked_argument_by_argument(m, call):
                 assert str(e).startswith(name + ":"), (what, e)
             else:
                 raise AssertionError(f"{call}: {name} ({what}) was accepted: {rc}")
+
+
+UNKNOWN_SIZE = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.fx.experimental.symbolic_shapes import ShapeEnv
+from tests.test_attn_binding_cpu import CALLS, fake, N, DIM
+from sparse_moe_expert_gemv_b200 import binding
+m = binding._marshal()
+mode = FakeTensorMode(shape_env=ShapeEnv())
+for heads, run in CALLS.values():
+    good = {name: fake((N, h, DIM)) for name, h in heads.items()}
+    for name, h in heads.items():
+        with mode:
+            bad = torch.empty((mode.shape_env.create_unbacked_symint(), h, DIM), dtype=torch.bfloat16,
+                              device="cuda:0")
+        try:
+            run(m, {**good, name: bad})
+        except ValueError as e:
+            assert "plain CUDA tensor" in str(e), e
+        else:
+            raise AssertionError(name)
+print("refused")
+"""
+
+
+def test_a_tensor_that_throws_is_a_python_error(m):
+    """Sizes that are no numbers: in a process of its own, which an exception
+    through the interpreter's C frames would end."""
+    r = subprocess.run([sys.executable, "-c", UNKNOWN_SIZE], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("refused"), (r.returncode, r.stderr[-2000:])
