@@ -179,10 +179,14 @@ MOE_DEV bool mbar_wait_live(uint32_t bar, uint32_t parity, const int *dead) {
 }
 // The same for a whole warp: one lane polls.  (32 lanes polling one barrier
 // are served one after another and hold up every other barrier of the SM.)
+// The shuffle hands the result on but orders no memory: the other lanes touch
+// what the barrier guards only behind the __syncwarp.
 MOE_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, const int *dead) {
   int ok = 0;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait_live(bar, parity, dead);
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
 }
 MOE_DEV void bar_sync_n(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 MOE_DEV void tma_box_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t policy) {
