@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     }
     __syncwarp();
     if (need) tma_load_2d(kfirst + box_at, &kmap, my_half * 64, y, q_bar);
-    int issued = 0, edge_uses = 0;
+    int issued = 0, edge_issued = 0, edge_uses = 0;
     for (int j = 0; j < n_tiles; ++j) {
       const int key0 = key_of(j);
       need_k = false;
@@ -400,8 +400,10 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       if (need) tma_load_2d(dst + box_at, &vmap, my_half * 64, y, bar);
       if (need_k) tma_load_2d(dst + C::TILE + box_at, &kmap, my_half * 64, y_k, full);
       ++issued;
+      edge_issued += edge;
       if (edge) {
-        ok = mbar_wait_warp(bar, edge_uses & 1, nullptr);
+        ok = mbar_wait_warp(bar, edge_uses & 1, &sh.dead);
+        if (!ok) break;  // not in order: nobody is told to read this tile
         ++edge_uses;
         for (int r = lane; r < kApTile; r += 32) {
           if (seen_by_some(key0 + r)) continue;
@@ -422,6 +424,16 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     if (!ok && lane == 0) give_up();
     // no tile may land after the block has gone
     (void)mbar_wait_bounded(q_bar, 0);
+    if (edge_uses < edge_issued) {
+      // given up on an edge tile: its pair's barrier still waits for this
+      // warp's arrival, which the values' landing stands in for
+      if (mbar_wait_bounded(smem_addr(&sh.edge), edge_uses & 1)) {
+        if (lane == 0) mbar_arrive(smem_addr(&sh.kv_full[(issued - 1) % C::PAIRS]));
+        __syncwarp();
+      } else {
+        --issued;
+      }
+    }
     for (int j = max(0, issued - C::PAIRS); j < issued; ++j)
       (void)mbar_wait_bounded(smem_addr(&sh.kv_full[j % C::PAIRS]), (j / C::PAIRS) & 1);
     }
