@@ -40,6 +40,11 @@ constexpr int kAtThreads = (kAtWarps + 1) * 32;
 constexpr int kAtStages = 3;
 constexpr int kAtMaxRows = 64;   // rows of a block (MT = 4)
 constexpr float kAtSlack = 8.f;  // log2 of the growth that o is not rescaled for
+// log2 of the largest term over an e4m3 cache, whose terms are fp16: with the
+// slack they reach 2^15, and what fp16 cannot hold starts 2^-32 below the
+// largest (2^-25 without: the 2^20 keys of a long flat tail lose up to 3 % of
+// the sum that way).  o and its sum carry the same factor.
+constexpr float kAtLift = 7.f;
 
 template <int D, bool FP8>
 struct AttnCfg {
@@ -620,7 +625,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         }
         // ---- running maximum and sum.  The terms are scaled by a reference
         // that follows the maximum only when it fell kAtSlack behind (p then
-        // holds values up to 2^kAtSlack): o is rarely rescaled
+        // holds values up to 2^kAtSlack, over e4m3 2^(kAtSlack + kAtLift)):
+        // o is rarely rescaled
         float corr[2] = {1.f, 1.f}, neg[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -635,7 +641,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
             corr[i] = ex2(m_run[i] - mx);
             m_run[i] = mx;
           }
-          neg[i] = m_run[i] == -INFINITY ? 0.f : -m_run[i];  // nothing seen yet: every p below is 2^-inf = 0
+          // nothing seen yet: every p below is 2^-inf = 0
+          neg[i] = m_run[i] == -INFINITY ? 0.f : (FP8 ? kAtLift : 0.f) - m_run[i];
         }
         float sum[2] = {0.f, 0.f};
 #pragma unroll
