@@ -299,6 +299,10 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
   const long long seen_lo = p.window > 0 ? (long long)pos0 - p.window + 1 : 0;
   const int sink_end = seen_lo > 0 ? (int)min((long long)p.n_sink, seen_lo) : 0;
   auto seen_by_some = [&](int k) { return k < s.kv && (k < sink_end || k >= seen_lo); };
+  // whether a tile from key0 on holds such rows (key0 + kApTile may be 2^31)
+  auto edge_tile = [&](int key0) {
+    return key0 > s.kv - kApTile || (key0 < seen_lo && key0 > sink_end - kApTile);
+  };
   if (wid == 8) {
     // ---------------------------------------------------------- producer
     few_registers();
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
       need_k = false;
       if (j + 1 < n_tiles) box_of(j + 1, need_k, y_k);
       const int st = j % C::PAIRS, use = j / C::PAIRS;
-      const bool edge = key0 + kApTile > s.kv || (key0 < seen_lo && key0 + kApTile > sink_end);
+      const bool edge = edge_tile(key0);
       const uint32_t bytes_v = bytes_of(need), bytes_k = bytes_of(need_k);
       if (use > 0) ok = mbar_wait_warp(smem_addr(&sh.kv_empty[st]), (use - 1) & 1, &sh.dead);
       if (!ok) break;
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
         ok = mbar_wait_warp(smem_addr(&sh.raw_full[st]), j & 1, &sh.dead);
         if (ok) {
           const int key0 = key_of(j);
-          const bool edge = is_v && (key0 + kApTile > s.kv || (key0 < seen_lo && key0 + kApTile > sink_end));
+          const bool edge = is_v && edge_tile(key0);
 #pragma unroll 2
           for (int r = (tid & 127) / (D / 16); r < kApTile; r += 128 / (D / 16)) {
             uint4 v = lds_u4(raw0 + st * C::RAW + r * D + c16 * 16);

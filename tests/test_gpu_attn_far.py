@@ -69,3 +69,38 @@ def test_a_long_flat_tail_behind_one_large_score(B, make_ctx, e4m3):
         tol = terms + want * (2.0 ** -7 + 2.0 ** -9 + 2.0 ** -8)
         assert (got.double() - want).abs().max() <= tol, (
             float(got.double().min()), float(got.double().max()), want, tol)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", [3, 70])
+def test_the_last_positions_below_2_31(B, make_ctx, e4m3, rows):
+    """A sequence of almost 2^31 tokens with a sliding window and sinks: only
+    its first and last pages are there, and what lies behind its end is NaN."""
+    n_q, n_kv, dim, page, window, sinks, near = 4, 2, 128, 64, 100, 5, 6
+    kv, most = 2 ** 31 - 100, 2 ** 25 - 1
+    ctx = make_ctx(n_q, n_kv, dim, page, e4m3)
+    # the same rows see the same keys in a short sequence without the pages between
+    n_pages = -(-kv // page)
+    short = A.Cache([kv - (n_pages - near - 1) * page], n_kv, dim, page, e4m3, seed=4)
+    table = torch.full((1, most), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = short.pages[0][0]
+    table[0, n_pages - near:n_pages] = ints(short.pages[0][1:])
+    batch = B.KvBatch(short.k, short.v, table, ints([0, rows]), ints([kv]), rows, k_scale=short.k_scale,
+                      v_scale=short.v_scale)
+    qkv = torch.randn((rows, n_q + 2 * n_kv, dim), device="cuda",
+                      generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+    q, k, v = qkv[:, :n_q], qkv[:, n_q:n_q + n_kv], qkv[:, n_q + n_kv:]
+    out = torch.full((rows, n_q, dim), float("nan"), dtype=torch.bfloat16, device="cuda")
+    B.moe_kv_append(ctx, batch, None, k, v, None, None, None)
+    B.moe_attn_prefill(ctx, batch, q, rows, 0.09, window, sinks, out)
+    B.moe_sync(ctx, 60000)
+    for which, x, scale in (("k", k, short.k_scale), ("v", v, short.v_scale)):
+        stored = short.rows64(0, which)[-rows:]
+        if e4m3:  # one rounding, and one of x / scale before it
+            tol = x.double().abs() * 2.0 ** -4 * (1 + 2.0 ** -19) + 2.0 ** -10 * scale.double()[:, None]
+            assert ((stored - x.double()).abs() <= tol).all()
+        else:
+            assert torch.equal(stored, x.double())
+    want, tol = A.attention64(q.contiguous(), short, [rows], 0.09, window, sinks,
+                              chunk=rows * (n_q // n_kv) > 64)
+    assert ((out.double() - want).abs() <= tol).all(), float((out.double() - want).abs().max())
