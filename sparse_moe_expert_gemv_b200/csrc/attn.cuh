@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!row_ok[i]) continue;
-          const float inv = l_run[i] > 0.f || l_run[i] != l_run[i] ? vs / l_run[i] : 0.f;
+          const float inv = vs / l_run[i];
           uint16_t *dst = p.out + row_o[i];
           if (FP8) {
 #pragma unroll
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
                 acc[2] += e * v[i][k].z;
                 acc[3] += e * v[i][k].w;
               }
-              store(it / (D / 4), it % (D / 4) * 4, acc, l > 0.f || l != l ? vs / l : 0.f);
+              store(it / (D / 4), it % (D / 4) * 4, acc, vs / l);
             }
           }
         };
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
                 l += e * __ldcg(slot_of(first + i) + RB * D + RB + r0 + r);
               }
               l = warp_sum(l);
-              if (lane == 0) inv[r] = l > 0.f || l != l ? vs / l : 0.f;
+              if (lane == 0) inv[r] = vs / l;
             }
             bar_sync_n(1, kAtWarps * 32);
             for (int it = tid; it < nr * (D / 4); it += kAtWarps * 32) {

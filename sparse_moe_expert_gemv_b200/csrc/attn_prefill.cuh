@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
     if (parts == 1) {
       if (ok) {
         tc_fence_after();
-        const float inv = l_run > 0.f || l_run != l_run ? vs / l_run : 0.f;
+        const float inv = vs / l_run;
         // Each warp turns its 32 rows in the place of its queries (every
         // product that reads them is through), so that whole rows leave at a
         // time: a thread's own row in 16-byte pieces would touch 32 lines a
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(AttnPfCfg<D, FP8>::THREADS, 1)
               acc[c][4 * e + 3] += f * v.w;
             }
         }
-        const float inv = l > 0.f || l != l ? vs / l : 0.f;
+        const float inv = vs / l;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
 #pragma unroll

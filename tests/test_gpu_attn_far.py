@@ -104,3 +104,26 @@ def test_the_last_positions_below_2_31(B, make_ctx, e4m3, rows):
     want, tol = A.attention64(q.contiguous(), short, [rows], 0.09, window, sinks,
                               chunk=rows * (n_q // n_kv) > 64)
     assert ((out.double() - want).abs() <= tol).all(), float((out.double() - want).abs().max())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows,kv", [(1, 40), (1, 9000), (40, 40), (40, 9000)])
+def test_scores_without_a_finite_value(B, make_ctx, e4m3, rows, kv):
+    """A row whose visible scores are all -inf has no softmax: NaN, as the
+    formula gives, not zeros; other rows are what they were."""
+    n_q, n_kv, dim = 8, 2, 64
+    ctx = make_ctx(n_q, n_kv, dim, 16, e4m3)
+    cache = A.Cache([kv, 90], n_kv, dim, 16, e4m3, seed=6)
+    A.as_bytes(cache.k)[cache.pages[0], ..., 0] = A.as_bytes(torch.tensor(-1.0, device="cuda").to(cache.k.dtype))
+    q = torch.randn((rows + 1, n_q, dim), device="cuda",
+                    generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+    poisoned = q.clone()
+    poisoned[rows - 1, 3, 0] = math.inf
+    out = torch.zeros_like(q)
+    B.moe_attn_prefill(ctx, cache.batch(B, [rows, 1]), poisoned, rows, 0.1, 0, 0, out)
+    B.moe_sync(ctx, 60000)
+    assert out[rows - 1, 3].isnan().all()
+    want, tol = A.attention64(q, cache, [rows, 1], 0.1, 0, 0, chunk=rows * (n_q // n_kv) > 64)
+    rest = torch.ones((rows + 1, n_q), dtype=torch.bool, device="cuda")
+    rest[rows - 1, 3] = False
+    assert ((out.double() - want).abs() <= tol)[rest].all()
