@@ -467,7 +467,11 @@ def _marshal():
     """The compiled marshalling of the attention calls, given their addresses."""
     import torch  # noqa: F401  (its libraries first)
 
-    from . import _marshal as m
+    try:
+        from . import _marshal as m
+    except ImportError as e:
+        raise ImportError("_marshal.so is missing or of another torch: build it with "
+                          "`python -m sparse_moe_expert_gemv_b200.build`") from e
     m.set_calls(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         _lib.moe_qk_norm_rope, _lib.moe_kv_append, _lib.moe_attn_forward, _lib.moe_attn_prefill)))
     return m
