@@ -121,6 +121,8 @@ class PagedKV:
         """The library's view of this layer's cache for calls of n_rows rows."""
         key = (layer, n_rows)
         if key not in self._batches:
+            if len(self._batches) >= 16 * len(self.k):  # prompts come in any number of rows
+                self._batches.clear()
             ks, vs = self.scales
             self._batches[key] = self.B.KvBatch(self.k[layer], self.v[layer], self.table, self.row_off, self.kv_len,
                                                 n_rows, k_scale=ks, v_scale=vs)

@@ -121,3 +121,18 @@ def test_steps_trims_and_refusals_at_random():
 def check_given(kv, n_pages):
     used = [p for s in kv.pages for p in s if p >= 0]
     assert sorted(used + kv._free) == list(range(n_pages))
+
+
+def test_batches_of_many_row_counts_are_not_all_kept():
+    class B:
+        MOE_KV_BF16 = MOE_KV_E4M3 = 1
+        moe_attn_configure = staticmethod(lambda *a: None)
+        KvBatch = staticmethod(lambda *a, **kw: a)
+
+    kv = PagedKV(B, None, n_layers=3, n_q=2, n_kv=1, head_dim=64, page_size=16, n_pages=4, max_seqs=1, max_len=64,
+                 device="cpu")
+    for n in range(1, 500):
+        for layer in range(3):
+            batch = kv.batch(layer, n)
+            assert batch[0] is kv.k[layer] and batch[-1] == n and kv.batch(layer, n) is batch
+        assert len(kv._batches) <= 48
