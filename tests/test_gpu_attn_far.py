@@ -127,3 +127,37 @@ def test_scores_without_a_finite_value(B, make_ctx, e4m3, rows, kv):
     rest = torch.ones((rows + 1, n_q), dtype=torch.bool, device="cuda")
     rest[rows - 1, 3] = False
     assert ((out.double() - want).abs() <= tol)[rest].all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_cache_past_2_31_elements(B, make_ctx, e4m3):
+    """Pages whose elements lie past 2^31 (bf16) and 2^32 bytes into the cache:
+    append, window and chunk attention."""
+    n_q, n_kv, dim, page = 4, 2, 128, 64
+    n_pages = (2 ** 32 if e4m3 else 2 ** 31) // (n_kv * page * dim) + 4000
+    ctx = make_ctx(n_q, n_kv, dim, page, e4m3)
+    rows = [3, 0, 70]
+    small = A.Cache([200, 30, 333], n_kv, dim, page, e4m3, seed=8)
+    k, v = (torch.empty((n_pages, *t.shape[1:]), dtype=t.dtype, device="cuda") for t in (small.k, small.v))
+    at = n_pages - 1 - 100 * torch.arange(small.k.shape[0], device="cuda")  # where the small cache's pages lie
+    assert int(at.min()) * n_kv * page * dim * k.element_size() > 2 ** 32
+    A.as_bytes(k)[at], A.as_bytes(v)[at] = A.as_bytes(small.k), A.as_bytes(small.v)
+    table = torch.where(small.table >= 0, at[small.table.clamp(min=0).long()].int(), -1)
+    n = sum(rows)
+    batch = B.KvBatch(k, v, table, ints([0, 3, 3, n]), ints(small.kv), n, k_scale=small.k_scale,
+                      v_scale=small.v_scale)
+    qkv = torch.randn((n, n_q + 2 * n_kv, dim), device="cuda",
+                      generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+    q, new_k, new_v = qkv[:, :n_q], qkv[:, n_q:n_q + n_kv], qkv[:, n_q + n_kv:]
+    B.moe_kv_append(ctx, batch, None, new_k, new_v, None, None, None)
+    same = small.batch(B, rows)  # the same append among few pages
+    B.moe_kv_append(ctx, same, None, new_k, new_v, None, None, None)
+    B.moe_sync(ctx, 60000)
+    for big, few in ((k, small.k), (v, small.v)):
+        assert torch.equal(A.as_bytes(big)[at].view(torch.uint8), A.as_bytes(few).view(torch.uint8))
+    for max_T in (3, 70):  # the window and the chunk kernel
+        out = torch.full((n, n_q, dim), float("nan"), dtype=torch.bfloat16, device="cuda")
+        B.moe_attn_prefill(ctx, batch, q, max_T, 0.09, 0, 0, out)
+        B.moe_sync(ctx, 60000)
+        want, tol = A.attention64(q.contiguous(), small, rows, 0.09, 0, 0, chunk=max_T * (n_q // n_kv) > 64)
+        assert ((out.double() - want).abs() <= tol).all(), float((out.double() - want).abs().max())
