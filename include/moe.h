@@ -344,8 +344,8 @@ MOE_API moe_status moe_ep_combine(moe_ctx *ctx, int N, const float *w_dev, const
  * one or many); kv_len[b] counts the sequence's tokens, these rows included,
  * so row t of T sits at position kv_len[b] - T + t.  The tables are device
  * data, read when the kernels run: a captured graph replays with whatever
- * they hold then.  Rows from row_off[n_seqs] on belong to no sequence and are
- * left as they were.  The device checks what it reads: a page id outside
+ * they hold then.  Rows before row_off[0] and from row_off[n_seqs] on belong
+ * to no sequence and are left as they were.  The device checks what it reads: a page id outside
  * [0, n_pages), or offsets and lengths that contradict each other or the
  * sizes given here, index nothing out of range, leave the rows concerned
  * unwritten (or, for a page that is only read, unspecified; where offsets

@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(kv_threads(ROWS)) kv_rows_kernel(KvRowsParams 
       long long at = -1;
       if (b < p.n_seqs) {
         const SeqView s = seq_view(p.row_off, p.kv_len, b, p.n_rows, p.max_pages, p.page);
-        if (!s.ok || row < s.row0 || row >= s.row0 + s.rows) {
+        if (!s.ok || row >= s.row0 + s.rows || (row < s.row0 && b > 0)) {
           atomicOr(p.status, kErrBadBatch);
-        } else {
+        } else if (row >= s.row0) {  // (rows in front of the first sequence are nobody's)
           pos = s.kv - s.rows + (row - s.row0);
           const int pg = __ldg(p.page_table + (long long)b * p.max_pages + pos / p.page);
           if ((unsigned)pg < (unsigned)p.n_pages)

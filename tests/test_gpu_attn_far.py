@@ -161,3 +161,40 @@ def test_a_cache_past_2_31_elements(B, make_ctx, e4m3):
         B.moe_sync(ctx, 60000)
         want, tol = A.attention64(q.contiguous(), small, rows, 0.09, 0, 0, chunk=max_T * (n_q // n_kv) > 64)
         assert ((out.double() - want).abs() <= tol).all(), float((out.double() - want).abs().max())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", [[2, 0, 3], [0, 40, 2]])
+def test_rows_before_the_first_sequence(B, make_ctx, e4m3, rows):
+    """Two batches may share one buffer of rows: offsets need not begin at 0.
+    Rows of no sequence, in front and behind, are left and are no error."""
+    n_q, n_kv, dim, page = 8, 2, 64, 16
+    ctx = make_ctx(n_q, n_kv, dim, page, e4m3)
+    cache = A.Cache([30, 7, 50] if rows[1] == 0 else [30, 70, 50], n_kv, dim, page, e4m3, seed=8)
+    front, behind, n = 5, 2, sum(rows)
+    batch = cache.batch(B, rows, front + behind)
+    batch.tensors[3].add_(front)
+    qkv = torch.randn((front + n + behind, n_q + 2 * n_kv, dim), device="cuda",
+                      generator=torch.Generator(device="cuda").manual_seed(5)).bfloat16()
+    q, k, v = qkv[:, :n_q], qkv[:, n_q:n_q + n_kv], qkv[:, n_q + n_kv:]
+    q_out, out = (torch.full((front + n + behind, n_q, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+                  for _ in range(2))
+    B.moe_kv_append(ctx, batch, q, k, v, None, None, q_out)
+    B.moe_attn_prefill(ctx, batch, q_out, max(rows), 0.1, 0, 0, out)
+    B.moe_sync(ctx, 60000)
+    assert torch.equal(q_out[front:front + n], q[front:front + n])
+    for t in (q_out, out):
+        assert (t[:front] == 7).all() and (t[front + n:] == 7).all()
+    want, tol = A.attention64(q[front:front + n].contiguous(), cache, rows, 0.1, 0, 0,
+                              chunk=max(rows) * (n_q // n_kv) > 64)
+    assert ((out[front:front + n].double() - want).abs() <= tol).all()
+    at = front
+    for b, r in enumerate(rows):  # the appended keys are where the sequence has them
+        stored = cache.rows64(b, "k")[len(cache.rows64(b, "k")) - r:]
+        x = k[at:at + r].double()
+        if e4m3:
+            s = cache.k_scale.double()[:, None]
+            assert ((stored - x).abs() <= x.abs() * 2.0 ** -4 * (1 + 2.0 ** -19) + 2.0 ** -10 * s).all()
+        else:
+            assert torch.equal(stored, x)
+        at += r
