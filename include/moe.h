@@ -426,7 +426,8 @@ MOE_API moe_status moe_kv_append(moe_ctx *ctx, const moe_kv_batch *batch, const 
  * where an e4m3 cache is read for at most 64 rows, max_T * n_q / n_kv, of a
  * KV head).  Cache rows that no row of their sequence sees may
  * hold anything; a NaN or infinite value that some row sees may reach the
- * call's other rows of that sequence.  The cache's length is split over the
+ * call's other rows of that sequence.  A row whose scores are all -infinity
+ * is NaN.  The cache's length is split over the
  * GPU and joined within the launch; results do not depend on timing.  A
  * sequence with more rows than max_T is served correctly, only slower.
  * Errors: INVALID_ARG, STATE, NOT_SUPPORTED (2^31 or more cache rows). */

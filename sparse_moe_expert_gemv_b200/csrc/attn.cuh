@@ -18,11 +18,14 @@
 // swizzle, one box per page), four warps compute on mma.sync fragments.  A
 // window has at most a few dozen rows per KV head, too few for a 128-row
 // tcgen05 tile, and the kernel is bound by reading the cache: 64 sequences of
-// one token over 32768 keys, 16 heads over 2 of 128, 309 us, 6.9 TB/s.  With
-// less to read, other costs show: one such sequence with 4 KV heads 21 us (10
-// of reading, the rest start, hand-over and joining), 64 ragged windows of up
-// to 5 rows over up to 4096 keys 52 us (34 of reading; two row tiles, and a
-// warp's chain of a tile is longer than its loading).
+// one token over 32768 keys, 16 heads over 2 of 128, 305 to 319 us from box to
+// box, 6.7 to 7.0 TB/s (over e4m3, half the bytes, 248 us: 4.3 TB/s, a warp's
+// chain of a tile and the conversions).  With less to read, other costs show:
+// one such sequence with 4 KV heads 21 us (10 of reading, the rest start,
+// hand-over and joining), 64 ragged windows of up to 5 rows over up to 4096
+// keys 52 us (34 of reading; two row tiles, and a warp's chain of a tile is
+// longer than its loading), 16 windows of 16 rows over 8000 keys 93 us (40 of
+// reading; four row tiles, whose registers spill).
 #pragma once
 
 #include <cuda.h>
@@ -182,8 +185,9 @@ MOE_DEV bool mbar_wait_live(uint32_t bar, uint32_t parity, const int *dead) {
   }
   return false;
 }
-// The same for a whole warp: one lane polls.  (32 lanes polling one barrier
-// are served one after another and hold up every other barrier of the SM.)
+// The same for a warp off the tiles' chain: one lane polls.  (32 lanes polling
+// one barrier are served one after another and hold up the SM's other
+// barriers, which matters where a warp waits most of its time.)
 // The shuffle hands the result on but orders no memory: the other lanes touch
 // what the barrier guards only behind the __syncwarp.
 MOE_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, const int *dead) {
@@ -286,7 +290,12 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     k = (int)(x - q * nt);
   };
   if (p.n_seqs <= 32) {
-    // few sequences: every warp finds the place for itself, a lane per sequence
+    // Few sequences: every warp finds the place for itself, a lane per
+    // sequence, and what few long segments need is looked for below.  Without
+    // all that, by the plain cut of the other branch: one token over 32768 keys
+    // 24.2 us against 21.5, 8 sequences over up to 8192 23.4 against 20.2, 32
+    // over up to 4096 33.3 against 32.0 (32 over 32768 keys 160 against 162).
+    // More sequences than lanes gain less and less, and take the plain cut.
     SeqView s{0, 0, 0, true};
     SeqTiles t{0, 0, 0};
     if (lane < p.n_seqs) {
@@ -516,7 +525,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     }
     // Q fragments.  An e4m3 cache computes in fp16: its values are exact
     // there, and each query row is divided by a power of two near its
-    // largest element, which rounds nothing that bf16 held above 2^-24 of it.
+    // largest element: exact for what bf16 holds above 2^-14 of that, and
+    // rounded by at most 2^-25 of it below.
     uint32_t qf[D / 16][4];
     float row_scale[2] = {p.scale_log2, p.scale_log2};
 #pragma unroll
@@ -576,6 +586,10 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
     for (int k = k_beg; k < k_end; ++k) {
+      // All lanes wait here, and in the rows' wait of the chunk kernel: with one
+      // that polls for the others, every tile waits for the shuffle too (one
+      // token over 32768 keys 21.7 against 21.2 us, 64 tokens 320 against 312,
+      // 8192 rows over 16384 keys 775 against 725 us).
       live = live && mbar_wait_live(smem_addr(&sh.full[st]), phase, &sh.dead);
       live = __all_sync(0xffffffffu, live);
       if (live) {

@@ -35,7 +35,9 @@
 // reaches two thirds of the special function unit's rate), hand-over 230, P V
 // and S 990, commit 360 -- of which the tensor cores work 2,048 for the two
 // tiles.  8192 rows of 16 heads over 16384 keys: 782 us, 1.05 PFLOP/s, the
-// blocks of the last incomplete wave splitting their keys (812 us without).
+// blocks of the last incomplete wave splitting their keys (812 us without); 680
+// to 793 us from box to box.  Over e4m3 875 us: four more warps convert every
+// tile, and the rows' threads spill (72 bytes at the launch's 128 registers).
 // Measured at earlier stages and not kept: two warps per row (927 against 900
 // us), scores double-buffered in steps of 64 keys (876 against 845 us: an MMA
 // of 64 columns takes as long as one of 128), exponentials on the FMA units by

@@ -67,7 +67,7 @@ class PagedKV:
     def step(self, rows):
         """Opens a step: rows[s] new tokens of sequence slot s (the batch's
         rows in slot order).  Gives them pages and brings the device tables up
-        to date.  Raises MemoryError, opening no step, when there are not enough
+        to date.  Raises MemoryError, changing nothing, when there are not enough
         pages."""
         if len(rows) != self.max_seqs or any(r < 0 for r in rows):
             raise ValueError(f"rows: one count for each of {self.max_seqs} slots")
